@@ -30,6 +30,9 @@ __all__ = [
     "ba_gdpa_cross_workspace_size", "ba_gdpa_cross_fwd", "ba_gdpa_cross_bwd", "gdpa_cross_fwd", "gdpa_cross_bwd",
     "ba_mx_quantize", "ba_mx_fwd_workspace_size", "ba_mx_fwd", "mx_quantize", "mx_block_attention_fwd",
     "ba_mx_bwd_workspace_size", "ba_mx_bwd", "mx_block_attention_bwd",
+    "HistoryCache", "ba_cache_write", "ba_cache_read", "ba_cache_summarize", "ba_cache_select", "ba_cache_fwd",
+    "ba_cache_fwd_workspace_size", "cache_write", "cache_read", "cache_summarize", "cache_select",
+    "cache_attention_fwd",
     "library_path",
 ]
 
@@ -51,6 +54,13 @@ class BAProblem(ctypes.Structure):
 class BARope(ctypes.Structure):
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int32),
                 ("q_rot", ctypes.c_void_p), ("k_rot", ctypes.c_void_p)]
+
+
+class BACache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class BAError(RuntimeError):
@@ -130,6 +140,19 @@ def _load():
     lib.ba_mx_bwd_workspace_size.restype = ctypes.c_size_t
     lib.ba_mx_bwd.argtypes = [prob, P, P, P, P, P, P, P, i32, i32, P, P, P, P, P, ctypes.c_size_t, P]
     lib.ba_mx_bwd.restype = ctypes.c_int
+    cache = ctypes.POINTER(BACache)
+    lib.ba_cache_write.argtypes = [cache, ctypes.c_int, P, P, P, P, i32, P]
+    lib.ba_cache_write.restype = ctypes.c_int
+    lib.ba_cache_read.argtypes = [cache, ctypes.c_int, P, P, i32, P, P, P]
+    lib.ba_cache_read.restype = ctypes.c_int
+    lib.ba_cache_summarize.argtypes = [cache, P, P, P, P]
+    lib.ba_cache_summarize.restype = ctypes.c_int
+    lib.ba_cache_select.argtypes = [cache, prob, P, P, P, P, P, i32, i32, i32, P, P]
+    lib.ba_cache_select.restype = ctypes.c_int
+    lib.ba_cache_fwd_workspace_size.argtypes = [cache, prob, i32, i32]
+    lib.ba_cache_fwd_workspace_size.restype = ctypes.c_size_t
+    lib.ba_cache_fwd.argtypes = [cache, prob, P, P, P, P, P, i32, P, i32, i32, P, P, P, ctypes.c_size_t, P]
+    lib.ba_cache_fwd.restype = ctypes.c_int
     rope = ctypes.POINTER(BARope)
     lib.ba_rope_fwd_workspace_size.argtypes = [prob, i32, i32]
     lib.ba_rope_fwd_workspace_size.restype = ctypes.c_size_t
@@ -688,3 +711,224 @@ def rope_block_attention_bwd(q, k, v, out, lse, dout, seq_offsets, block, window
     if st != BA_OK:
         raise BAError(st, "ba_rope_bwd")
     return dq, dk, dv
+
+
+# ------------------------------------------------------- history cache ---
+
+class HistoryCache:
+    """A paged cache of keys and values in MXFP8 (ba_cache in include/ba.h).
+
+    k, v: uint8 [num_pages, kv_heads, page_size, head_dim] (E4M3 codes);
+    k_scales, v_scales: uint8 [num_pages, kv_heads, page_size, head_dim / 32]
+    (E8M0 codes); page_table: int32 [batch, max_pages]; status: int32 CUDA
+    tensor of one word, zeroed here when not given. The tensors are kept, not
+    copied: the caller changes page_table in place as histories grow.
+    """
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "page_table", "status", "struct", "_ref", "batch", "device")
+
+    def __init__(self, k, v, k_scales, v_scales, page_table, status=None):
+        if k.dim() != 4:
+            raise ValueError("k must be [num_pages, kv_heads, page_size, head_dim]")
+        num_pages, kv_heads, page_size, head_dim = k.shape
+        if page_table.dim() != 2 or page_table.dtype != torch.int32:
+            raise ValueError("page_table must be int32 [batch, max_pages]")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        for name, t, shape in (("k", k, k.shape), ("v", v, k.shape),
+                               ("k_scales", k_scales, (*k.shape[:3], head_dim // 32)),
+                               ("v_scales", v_scales, (*k.shape[:3], head_dim // 32))):
+            if t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name} must be uint8 {list(shape)}")
+        if status.dtype != torch.int32 or status.numel() < 1:
+            raise ValueError("status must be an int32 tensor")
+        for name, t in (("k", k), ("v", v), ("k_scales", k_scales), ("v_scales", v_scales),
+                        ("page_table", page_table), ("status", status)):
+            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor on k's device")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.page_table, self.status = page_table, status
+        self.batch, self.device = page_table.shape[0], k.device
+        self.struct = BACache(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                              page_table.data_ptr(), status.data_ptr(), page_table.shape[0], page_table.shape[1],
+                              num_pages, page_size, kv_heads, head_dim)
+        self._ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, page_table):
+        """A cache of zeroed pages on page_table's device."""
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=page_table.device) for _ in "kv")
+        ks, vs = (torch.zeros((*shape[:3], head_dim // 32), dtype=torch.uint8, device=page_table.device) for _ in "kv")
+        return cls(k, v, ks, vs, page_table)
+
+
+def _cache_ref(cache):
+    return cache._ref if isinstance(cache, HistoryCache) else ctypes.byref(cache)
+
+
+def ba_cache_write(cache, dtype, k, v, row_offsets, starts, total_rows, stream=None) -> int:
+    """Direct call of the C entry point (cache: HistoryCache or BACache); returns its status code."""
+    return int(_load().ba_cache_write(_cache_ref(cache), int(dtype), _ptr(k), _ptr(v), _ptr(row_offsets),
+                                      _ptr(starts), int(total_rows), _stream(stream)))
+
+
+def ba_cache_read(cache, dtype, row_offsets, starts, total_rows, k, v, stream=None) -> int:
+    """Direct call of the C entry point; returns its status code."""
+    return int(_load().ba_cache_read(_cache_ref(cache), int(dtype), _ptr(row_offsets), _ptr(starts),
+                                     int(total_rows), _ptr(k), _ptr(v), _stream(stream)))
+
+
+def ba_cache_summarize(cache, starts, ends, summaries, stream=None) -> int:
+    """Direct call of the C entry point; returns its status code."""
+    return int(_load().ba_cache_summarize(_cache_ref(cache), _ptr(starts), _ptr(ends), _ptr(summaries),
+                                          _stream(stream)))
+
+
+def ba_cache_select(cache, problem, q, q_offsets, lens, positions, summaries, block, window, topk, page_mask,
+                    stream=None) -> int:
+    """Direct call of the C entry point; returns its status code."""
+    return int(_load().ba_cache_select(_cache_ref(cache), ctypes.byref(problem), _ptr(q), _ptr(q_offsets),
+                                       _ptr(lens), _ptr(positions), _ptr(summaries), int(block), int(window),
+                                       int(topk), _ptr(page_mask), _stream(stream)))
+
+
+def ba_cache_fwd_workspace_size(cache, problem: BAProblem, block: int, window: int) -> int:
+    return int(_load().ba_cache_fwd_workspace_size(_cache_ref(cache), ctypes.byref(problem), int(block), int(window)))
+
+
+def ba_cache_fwd(cache, problem, q, q_offsets, lens, positions, tree_mask, tree_words, page_mask, block, window, out,
+                 lse, workspace, workspace_bytes=None, stream=None) -> int:
+    """Direct call of the C entry point; returns its status code."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return int(_load().ba_cache_fwd(_cache_ref(cache), ctypes.byref(problem), _ptr(q), _ptr(q_offsets), _ptr(lens),
+                                    _ptr(positions), _ptr(tree_mask), int(tree_words), _ptr(page_mask), int(block),
+                                    int(window), _ptr(out), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+                                    _stream(stream)))
+
+
+def _check_cache_args(cache, named):
+    """(name, tensor, dtype, shape) of each argument: contiguous, on the cache's device, which is the current one
+    (the library launches on the current device)."""
+    dev = cache.device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}: make it the current device")
+    for name, t, dtype, shape in named:
+        if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
+
+
+def _cache_rows(cache, k, v, row_offsets, starts):
+    if k.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    s = cache.struct
+    shape = (k.shape[0], s.kv_heads, s.head_dim)
+    _check_cache_args(cache, (("k", k, k.dtype, shape), ("v", v, k.dtype, shape),
+                              ("row_offsets", row_offsets, torch.int32, (s.batch + 1,)),
+                              ("starts", starts, torch.int32, (s.batch,))))
+
+
+def cache_write(cache, k, v, row_offsets, starts, stream=None):
+    """Quantises the jagged rows of k and v [rows, kv_heads, head_dim] (bf16 or
+    float32) into the cache: row t of sequence b goes to slot starts[b] + t
+    (ba_cache_write)."""
+    _cache_rows(cache, k, v, row_offsets, starts)
+    st = ba_cache_write(cache, _DTYPES[k.dtype], k, v, row_offsets, starts, k.shape[0], stream)
+    if st != BA_OK:
+        raise BAError(st, "ba_cache_write")
+
+
+def cache_read(cache, row_offsets, starts, total_rows, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """Slots back as dense, jagged rows (k, v) [total_rows, kv_heads, head_dim]:
+    row t of sequence b is slot starts[b] + t (ba_cache_read). Allocates k and
+    v with torch unless both are given."""
+    if (k is None) != (v is None):
+        raise ValueError("pass both k and v, or neither")
+    if k is None:
+        s = cache.struct
+        k, v = (torch.empty((total_rows, s.kv_heads, s.head_dim), dtype=dtype, device=cache.device) for _ in "kv")
+    _cache_rows(cache, k, v, row_offsets, starts)
+    if k.shape[0] != total_rows:
+        raise ValueError(f"k and v must have {total_rows} rows")
+    st = ba_cache_read(cache, _DTYPES[k.dtype], row_offsets, starts, total_rows, k, v, stream)
+    if st != BA_OK:
+        raise BAError(st, "ba_cache_read")
+    return k, v
+
+
+def cache_summarize(cache, starts, ends, summaries, stream=None):
+    """Mean keys of the full pages that hold a slot in [starts[b], ends[b]) into
+    summaries, float32 [num_pages, kv_heads, head_dim] (ba_cache_summarize)."""
+    s = cache.struct
+    _check_cache_args(cache, (("starts", starts, torch.int32, (s.batch,)), ("ends", ends, torch.int32, (s.batch,)),
+                              ("summaries", summaries, torch.float32, (s.num_pages, s.kv_heads, s.head_dim))))
+    st = ba_cache_summarize(cache, starts, ends, summaries, stream)
+    if st != BA_OK:
+        raise BAError(st, "ba_cache_summarize")
+    return summaries
+
+
+def _check_queries(cache, q, q_offsets, lens, positions):
+    s = cache.struct
+    if q.dim() != 3 or q.shape[1] % s.kv_heads:
+        raise ValueError("q must be [rows, heads, head_dim] with heads a multiple of the cache's kv_heads")
+    rows = q.shape[0]
+    named = [("q", q, torch.bfloat16, (rows, q.shape[1], s.head_dim)),
+             ("q_offsets", q_offsets, torch.int32, (s.batch + 1,)), ("lens", lens, torch.int32, (s.batch,))]
+    if positions is not None:
+        named.append(("positions", positions, torch.int32, (rows,)))
+    return rows, named
+
+
+def cache_select(cache, q, q_offsets, lens, summaries, block, window, topk, positions=None, page_mask=None,
+                 stream=None):
+    """The topk pages outside each query's window whose mean keys score highest,
+    as bits, int32 [rows, kv_heads, ceil(max_pages / 32)] (ba_cache_select);
+    allocates page_mask with torch."""
+    s = cache.struct
+    rows, named = _check_queries(cache, q, q_offsets, lens, positions)
+    words = (s.max_pages + 31) // 32
+    if page_mask is None:
+        page_mask = torch.empty((rows, s.kv_heads, words), dtype=torch.int32, device=cache.device)
+    named += [("summaries", summaries, torch.float32, (s.num_pages, s.kv_heads, s.head_dim)),
+              ("page_mask", page_mask, torch.int32, (rows, s.kv_heads, words))]
+    _check_cache_args(cache, named)
+    st = ba_cache_select(cache, make_problem(q, q_offsets), q, q_offsets, lens, positions, summaries, block, window,
+                         topk, page_mask, stream)
+    if st != BA_OK:
+        raise BAError(st, "ba_cache_select")
+    return page_mask
+
+
+def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None, tree_mask=None, page_mask=None,
+                        out=None, lse=None, workspace=None, stream=None):
+    """Attention of new events over the cache under the block rule (ba_cache_fwd):
+    one event a sequence, a chunk, a tree (tree_mask int32 [rows, words], and
+    positions) or candidates, with pages selected outside the window
+    (page_mask, from cache_select). Their own keys and values must be in the
+    slots from lens on. Allocates out/lse (and a workspace) with torch."""
+    s = cache.struct
+    rows, named = _check_queries(cache, q, q_offsets, lens, positions)
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2:
+            raise ValueError("tree_mask must be [rows, words]")
+        words = tree_mask.shape[1]
+        named.append(("tree_mask", tree_mask, torch.int32, (rows, words)))
+    if page_mask is not None:
+        named.append(("page_mask", page_mask, torch.int32, (rows, s.kv_heads, (s.max_pages + 31) // 32)))
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((q.shape[1], rows), dtype=torch.float32, device=q.device)
+    named += [("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (q.shape[1], rows))]
+    _check_cache_args(cache, named)
+    prob = make_problem(q, q_offsets)
+    if workspace is None:
+        workspace = workspace_for(ba_cache_fwd_workspace_size(cache, prob, block, window), q.device)
+    st = ba_cache_fwd(cache, prob, q, q_offsets, lens, positions, tree_mask, words, page_mask, block, window, out, lse,
+                      workspace, stream=stream)
+    if st != BA_OK:
+        raise BAError(st, "ba_cache_fwd")
+    return out, lse

@@ -12,8 +12,11 @@
 //           copies of q and k into the workspace before the attention
 //           kernels read them; the bf16 backward turns dq and dk back inside
 //           the dQ and dK/dV epilogues, the fp32 one in a pass after them
+//   ba_cache_*: one kernel each (ba_cache_fwd: the attention kernel, and a
+//           joining kernel when the slots were split)
 // Nothing here allocates, synchronises or falls back to another device.
 #include "ba.h"
+#include "ba_cache.cuh"
 #include "ba_common.cuh"
 #include "ba_kernels.cuh"
 
@@ -812,6 +815,199 @@ ba_status ba_mx_bwd(const ba_problem *p, const void *q, const void *k, const voi
                        workspace_bytes, stream);
 }
 
+// ------------------------------------------------------- history cache ---
+
+namespace {
+
+ba_status check_cache(const ba_cache *c, CacheView &view)
+{
+    if (!c) return BA_ERR_INVALID_ARG;
+    if (c->batch < 0 || c->max_pages < 1 || c->num_pages < 1 || c->kv_heads < 1 || c->head_dim < 1 ||
+        c->page_size < 1)
+        return BA_ERR_INVALID_ARG;
+    if (!c->k || !c->v || !c->k_scales || !c->v_scales || !aligned(c->k, 16) || !aligned(c->v, 16) ||
+        !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))
+        return BA_ERR_INVALID_ARG;
+    if ((c->batch > 0 && !c->page_table) || !aligned(c->page_table, 4) || !aligned(c->status, 4))
+        return BA_ERR_INVALID_ARG;
+    if (c->head_dim != 64 && c->head_dim != 128) return BA_ERR_UNSUPPORTED;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return BA_ERR_UNSUPPORTED;
+    // slots are numbered in 31 bits, heads are a grid dimension, (sequence, head) pairs too
+    if (int64_t(c->max_pages) * c->page_size > INT32_MAX || c->kv_heads > 65535 ||
+        int64_t(c->batch) * c->kv_heads > INT32_MAX)
+        return BA_ERR_UNSUPPORTED;
+    int shift = 4;
+    while ((1 << shift) < c->page_size) ++shift;
+    view = CacheView{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), static_cast<uint8_t *>(c->k_scales),
+                     static_cast<uint8_t *>(c->v_scales), c->page_table, c->status, c->batch, c->max_pages,
+                     c->num_pages, shift, c->kv_heads, c->head_dim};
+    return BA_OK;
+}
+
+// The dense side of ba_cache_write and ba_cache_read.
+ba_status check_rows(const ba_cache &c, ba_dtype dtype, const void *k, const void *v, const int32_t *row_offsets,
+                     const int32_t *starts, int32_t total_rows)
+{
+    if ((dtype != BA_F32 && dtype != BA_BF16) || total_rows < 0 || (c.batch == 0 && total_rows > 0))
+        return BA_ERR_INVALID_ARG;
+    if (total_rows == 0) return BA_OK;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !row_offsets || !aligned(row_offsets, 4) || !starts ||
+        !aligned(starts, 4))
+        return BA_ERR_INVALID_ARG;
+    if (int64_t(c.kv_heads) * c.head_dim > (int64_t(1) << 24)) return BA_ERR_UNSUPPORTED;
+    return BA_OK;
+}
+
+// The queries of ba_cache_select and ba_cache_fwd.
+ba_status check_queries(const ba_cache &c, const ba_problem *p, int32_t block, int32_t window)
+{
+    if (!p || p->batch < 0 || p->total_tokens < 0 || p->heads < 1 || p->head_dim < 1 || block < 1 || window < 1)
+        return BA_ERR_INVALID_ARG;
+    if ((p->dtype != BA_F32 && p->dtype != BA_BF16) || (p->batch == 0 && p->total_tokens != 0) ||
+        p->batch != c.batch || p->head_dim != c.head_dim || p->heads % c.kv_heads != 0)
+        return BA_ERR_INVALID_ARG;
+    if (p->dtype != BA_BF16) return BA_ERR_UNSUPPORTED;
+    if (int64_t(p->heads) * p->head_dim > (int64_t(1) << 24)) return BA_ERR_UNSUPPORTED;
+    // query rows of a head group, with a tile number for every sequence, are numbered in 31 bits
+    if (int64_t(p->total_tokens) * (p->heads / c.kv_heads) + p->batch > INT32_MAX) return BA_ERR_UNSUPPORTED;
+    return BA_OK;
+}
+
+ba_status need_b200(int &num_sms)
+{
+    int cc = 0;
+    if (!device_info(num_sms, cc)) return BA_ERR_CUDA;
+    return cc == 10 ? BA_OK : BA_ERR_UNSUPPORTED;
+}
+
+CacheFwdPlan plan_for(const ba_cache &c, const ba_problem &p, int32_t block, int32_t window, bool has_mask)
+{
+    return cache_fwd_plan(p.batch, p.total_tokens, c.kv_heads, p.heads / c.kv_heads, p.head_dim,
+                          int64_t(c.max_pages) * c.page_size, block, window, has_mask);
+}
+
+} // namespace
+
+ba_status ba_cache_write(const ba_cache *cache, ba_dtype dtype, const void *k, const void *v,
+                         const int32_t *row_offsets, const int32_t *starts, int32_t total_rows, ba_stream_t stream_)
+{
+    CacheView c;
+    ba_status st = check_cache(cache, c);
+    if (st != BA_OK || (st = check_rows(*cache, dtype, k, v, row_offsets, starts, total_rows)) != BA_OK) return st;
+    int num_sms = 0;
+    if (total_rows == 0) return BA_OK;
+    if ((st = need_b200(num_sms)) != BA_OK) return st;
+    BA_TRY(launch_cache_write(c, dtype == BA_F32, k, v, row_offsets, starts, total_rows, num_sms,
+                              reinterpret_cast<cudaStream_t>(stream_)));
+    return BA_OK;
+}
+
+ba_status ba_cache_read(const ba_cache *cache, ba_dtype dtype, const int32_t *row_offsets, const int32_t *starts,
+                        int32_t total_rows, void *k, void *v, ba_stream_t stream_)
+{
+    CacheView c;
+    ba_status st = check_cache(cache, c);
+    if (st != BA_OK || (st = check_rows(*cache, dtype, k, v, row_offsets, starts, total_rows)) != BA_OK) return st;
+    int num_sms = 0;
+    if (total_rows == 0) return BA_OK;
+    if ((st = need_b200(num_sms)) != BA_OK) return st;
+    BA_TRY(launch_cache_read(c, dtype == BA_F32, row_offsets, starts, total_rows, k, v, num_sms,
+                             reinterpret_cast<cudaStream_t>(stream_)));
+    return BA_OK;
+}
+
+ba_status ba_cache_summarize(const ba_cache *cache, const int32_t *starts, const int32_t *ends, float *summaries,
+                             ba_stream_t stream_)
+{
+    CacheView c;
+    ba_status st = check_cache(cache, c);
+    if (st != BA_OK) return st;
+    if (!summaries || !aligned(summaries, 16) ||
+        (c.batch > 0 && (!starts || !aligned(starts, 4) || !ends || !aligned(ends, 4))))
+        return BA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if (c.batch == 0) return BA_OK;
+    if ((st = need_b200(num_sms)) != BA_OK) return st;
+    BA_TRY(launch_cache_summarize(c, starts, ends, summaries, num_sms, reinterpret_cast<cudaStream_t>(stream_)));
+    return BA_OK;
+}
+
+ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, const void *q, const int32_t *q_offsets,
+                          const int32_t *lens, const int32_t *positions, const float *summaries, int32_t block,
+                          int32_t window, int32_t topk, uint32_t *page_mask, ba_stream_t stream_)
+{
+    CacheView c;
+    ba_status st = check_cache(cache, c);
+    if (st != BA_OK || (st = check_queries(*cache, problem, block, window)) != BA_OK) return st;
+    const ba_problem &P = *problem;
+    if (topk < 1) return BA_ERR_INVALID_ARG;
+    if (c.max_pages > kSelectMaxPages) return BA_ERR_UNSUPPORTED;
+    if (P.total_tokens == 0) return BA_OK;
+    if (!q || !aligned(q, 16) || !q_offsets || !aligned(q_offsets, 4) || !lens || !aligned(lens, 4) ||
+        !aligned(positions, 4) || !summaries || !aligned(summaries, 16) || !page_mask || !aligned(page_mask, 4))
+        return BA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((st = need_b200(num_sms)) != BA_OK) return st;
+    const CacheQuery cq{static_cast<const __nv_bfloat16 *>(q), q_offsets, lens, positions, P.total_tokens,
+                        P.heads / c.kv_heads, block, window};
+    BA_TRY(launch_cache_select(c, cq, summaries, topk, page_mask, num_sms, reinterpret_cast<cudaStream_t>(stream_)));
+    return BA_OK;
+}
+
+size_t ba_cache_fwd_workspace_size(const ba_cache *cache, const ba_problem *problem, int32_t block, int32_t window)
+{
+    CacheView c;
+    if (check_cache(cache, c) != BA_OK || check_queries(*cache, problem, block, window) != BA_OK) return 0;
+    const size_t a = plan_for(*cache, *problem, block, window, false).bytes;
+    const size_t b = plan_for(*cache, *problem, block, window, true).bytes;
+    return a > b ? a : b;
+}
+
+ba_status ba_cache_fwd(const ba_cache *cache, const ba_problem *problem, const void *q, const int32_t *q_offsets,
+                       const int32_t *lens, const int32_t *positions, const uint32_t *tree_mask, int32_t tree_words,
+                       const uint32_t *page_mask, int32_t block, int32_t window, void *out, float *lse,
+                       void *workspace, size_t workspace_bytes, ba_stream_t stream_)
+{
+    CacheFwd f;
+    ba_status st = check_cache(cache, f.c);
+    if (st != BA_OK || (st = check_queries(*cache, problem, block, window)) != BA_OK) return st;
+    const ba_problem &P = *problem;
+    if (tree_words < 0 || (tree_mask && tree_words < 1)) return BA_ERR_INVALID_ARG;
+    if (P.total_tokens == 0) return BA_OK;
+    if (!q || !aligned(q, 16) || !q_offsets || !aligned(q_offsets, 4) || !lens || !aligned(lens, 4) ||
+        !aligned(positions, 4) || !aligned(tree_mask, 4) || !aligned(page_mask, 4) || !out || !aligned(out, 16) ||
+        !lse || !aligned(lse, 4))
+        return BA_ERR_INVALID_ARG;
+    const CacheFwdPlan plan = plan_for(*cache, P, block, window, page_mask != nullptr);
+    if (plan.bytes > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.bytes))
+        return BA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((st = need_b200(num_sms)) != BA_OK) return st;
+    f.q = CacheQuery{static_cast<const __nv_bfloat16 *>(q), q_offsets, lens, positions, P.total_tokens,
+                     P.heads / f.c.kv_heads, block, window};
+    f.tree = tree_mask;
+    f.page_mask = page_mask;
+    f.tree_words = tree_words;
+    f.mask_words = (f.c.max_pages + 31) / 32;
+    f.chunk = plan.chunk;
+    f.nsplit = plan.nsplit;
+    f.scale_log2 = float(1.4426950408889634 / std::sqrt(double(P.head_dim)));
+    f.out = static_cast<__nv_bfloat16 *>(out);
+    f.lse = lse;
+    f.part_ml = nullptr;
+    f.part_o = nullptr;
+    if (plan.nsplit > 1) {
+        const size_t parts = size_t(plan.nsplit) * size_t(P.total_tokens) * size_t(P.heads);
+        f.part_ml = static_cast<float2 *>(workspace);
+        f.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256(parts * sizeof(float2)));
+    }
+    BA_TRY(prof_mark(0, 0, reinterpret_cast<cudaStream_t>(stream_)));
+    BA_TRY(launch_cache_fwd(f, plan, reinterpret_cast<cudaStream_t>(stream_)));
+    BA_TRY(prof_mark(0, 1, reinterpret_cast<cudaStream_t>(stream_)));
+    return BA_OK;
+}
+
 ba_status ba_device_status(const void *workspace, ba_stream_t stream_)
 {
     if (!workspace) return BA_ERR_INVALID_ARG;
@@ -821,7 +1017,7 @@ ba_status ba_device_status(const void *workspace, ba_stream_t stream_)
         cudaStreamSynchronize(stream) != cudaSuccess)
         return BA_ERR_CUDA;
     if (word & kStatusTimeout) return BA_ERR_TIMEOUT;
-    return (word & kStatusRopeRange) ? BA_ERR_INVALID_ARG : BA_OK;
+    return (word & (kStatusRopeRange | kStatusCacheRange)) ? BA_ERR_INVALID_ARG : BA_OK;
 }
 
 ba_status ba_selftest_wait_timeout(void *workspace, size_t workspace_bytes, int32_t limit_us, ba_stream_t stream_)

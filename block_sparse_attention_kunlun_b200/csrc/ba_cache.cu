@@ -1,0 +1,531 @@
+// The history cache's memory-bound kernels (layout and format in ba_cache.cuh):
+//   cache_write_kernel      dense rows, quantised as they are written
+//   cache_read_kernel       slots back as dense rows
+//   cache_summarize_kernel  the mean key of each full page
+//   cache_select_kernel     the pages whose mean keys score highest for a query
+// "GEM (Meta)", section "Training infrastructure", has the jagged histories;
+// the pages do not describe how they are served.
+#include "ba_cache.cuh"
+#include "ba_kernels.cuh"
+#include "ba_ptx.cuh"
+
+namespace ba {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kRowsPerBlock = 32; // most dense rows a block takes
+
+// Pool rows (head 0) of `n` consecutive dense rows from row0 on. A row whose slot is
+// not in the cache gets -1.
+__device__ __forceinline__ void find_rows(const CacheView &c, const int32_t *row_offsets, const int32_t *starts,
+                                          int32_t row0, int32_t n, int64_t *target)
+{
+    if (int(threadIdx.x) < n) {
+        const int32_t row = row0 + threadIdx.x;
+        const int32_t b = sequence_of_row(row_offsets, c.batch, row);
+        const int64_t slot = int64_t(__ldg(starts + b)) + row - __ldg(row_offsets + b);
+        const int64_t pi = slot >> c.page_shift;
+        const int32_t id = slot >= 0 && pi < c.max_pages ? cache_page(c, b, int32_t(pi)) : -1;
+        if (id < 0) cache_range_error(c);
+        target[threadIdx.x] = id < 0 ? -1 : cache_row(c, id, 0, int32_t(slot & ((1 << c.page_shift) - 1)));
+    }
+    __syncthreads();
+}
+
+// Eight values from a dense row.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *x, float (&f)[8])
+{
+    const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(x));
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(ws[i] << 16);
+        f[2 * i + 1] = __uint_as_float(ws[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *x, float (&f)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4 *>(x)), b = __ldcs(reinterpret_cast<const float4 *>(x) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+} // namespace
+
+// Four consecutive lanes hold one 32-value block, eight values each: 16 (or 32) bytes in,
+// 8 bytes out per lane, so a warp reads 512 (1024) and writes 256 consecutive bytes. The
+// block's largest magnitude takes two shuffles; e = floor(log2 amax) - 8 is its exponent
+// field, and multiplying by 2^-e is exact in float32 (the quotient stays below 2^9; what
+// underflows is far below E4M3's smallest value), so the conversion to E4M3 is the only
+// rounding. fmaxf drops NaN: a NaN leaves its block's scale alone and becomes E4M3's NaN;
+// an infinity gives e = 120 and the largest code.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_write_kernel(const CacheView c, const T *__restrict__ k, const T *__restrict__ v,
+                       const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts, int32_t total_rows,
+                       int32_t rows_per_block)
+{
+    __shared__ int64_t target[kRowsPerBlock];
+    const int32_t row0 = blockIdx.x * rows_per_block;
+    const int32_t n = min(rows_per_block, total_rows - row0);
+    find_rows(c, row_offsets, starts, row0, n, target);
+    const int32_t D = c.head_dim, per_head = D / 8, per_row = c.kv_heads * per_head;
+    const int32_t units = n * per_row; // lanes of eight values; a multiple of 8 (D >= 64)
+    const bool values = blockIdx.y != 0;
+    const T *src = values ? v : k;
+    uint8_t *elems = values ? c.v : c.k, *scales = values ? c.v_scales : c.k_scales;
+    const int64_t base = int64_t(row0) * per_row;
+    const int32_t head_rows = 1 << c.page_shift;
+#pragma unroll 4
+    for (int32_t u0 = 0; u0 < units; u0 += kRowThreads) {
+        const int32_t u = u0 + threadIdx.x;
+        const bool live = u < units;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (live) load8(src + (base + u) * 8, f);
+        float amax = fmaxf(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))),
+                           fmaxf(fmaxf(fabsf(f[4]), fabsf(f[5])), fmaxf(fabsf(f[6]), fabsf(f[7]))));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t bits = __float_as_uint(amax);
+        // exponent code e + 127 = field - 8, not below 0 (subnormal maxima too); an all-zero block has e = -8
+        uint32_t code = bits >> 23;
+        code = amax > 0.f ? (code > 8 ? code - 8 : 0u) : 119u;
+        const float inv = __uint_as_float(code < 254 ? (254 - code) << 23 : 0x00400000u);
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            w[i] = lo | (hi << 16);
+        }
+        const int32_t r = u / per_row, x = u % per_row, h = x / per_head, d8 = x % per_head;
+        // the head's scale codes as one word (two or four bytes), gathered by its first lane
+        uint32_t word = code << (8 * (d8 / 4));
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        if (D == 128) word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        if (!live || target[r] < 0) continue;
+        const int64_t row = target[r] + int64_t(h) * head_rows;
+        *reinterpret_cast<uint2 *>(elems + row * D + d8 * 8) = make_uint2(w[0], w[1]);
+        if (d8 == 0) {
+            if (D == 128) *reinterpret_cast<uint32_t *>(scales + row * 4) = word;
+            else *reinterpret_cast<uint16_t *>(scales + row * 2) = uint16_t(word);
+        }
+    }
+}
+
+// Sixteen values a lane: 16 bytes of codes in, 32 (bf16) or 64 bytes out. A bf16 result is
+// exact (four significant bits) unless it falls below bf16's normal range.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_read_kernel(const CacheView c, const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts,
+                      int32_t total_rows, int32_t rows_per_block, T *__restrict__ k, T *__restrict__ v)
+{
+    __shared__ int64_t target[kRowsPerBlock];
+    const int32_t row0 = blockIdx.x * rows_per_block;
+    const int32_t n = min(rows_per_block, total_rows - row0);
+    find_rows(c, row_offsets, starts, row0, n, target);
+    const int32_t D = c.head_dim, per_head = D / 16, per_row = c.kv_heads * per_head;
+    const int32_t units = n * per_row;
+    const bool values = blockIdx.y != 0;
+    T *dst = values ? v : k;
+    const uint8_t *elems = values ? c.v : c.k, *scales = values ? c.v_scales : c.k_scales;
+    const int64_t base = int64_t(row0) * per_row;
+    const int32_t head_rows = 1 << c.page_shift;
+#pragma unroll 4
+    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
+        const int32_t r = u / per_row, x = u % per_row, h = x / per_head, d16 = x % per_head;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        float s = 0.f;
+        if (target[r] >= 0) {
+            const int64_t row = target[r] + int64_t(h) * head_rows;
+            w = __ldg(reinterpret_cast<const uint4 *>(elems + row * D) + d16);
+            s = mx_scale(__ldg(scales + row * (D / 32) + d16 / 2));
+        }
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t o[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
+            f.x *= s;
+            f.y *= s;
+            if (sizeof(T) == 2) {
+                o[i] = pack_bf16x2(f.x, f.y);
+            } else {
+                o[2 * i] = __float_as_uint(f.x);
+                o[2 * i + 1] = __float_as_uint(f.y);
+            }
+        }
+        uint4 *out = reinterpret_cast<uint4 *>(dst + (base + u) * 16);
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T)); ++i)
+            __stcs(out + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+    }
+}
+
+namespace {
+
+// Rows a block takes: enough blocks to fill the GPU when there are few rows (a step of
+// single events), up to 32 rows a block when there are many.
+int32_t rows_per_block(int32_t total_rows, int num_sms)
+{
+    const int64_t want = (int64_t(total_rows) + 2 * num_sms - 1) / (2 * num_sms);
+    return int32_t(want < 1 ? 1 : (want > kRowsPerBlock ? kRowsPerBlock : want));
+}
+
+} // namespace
+
+cudaError_t launch_cache_write(const CacheView &c, bool f32, const void *k, const void *v, const int32_t *row_offsets,
+                               const int32_t *starts, int32_t total_rows, int num_sms, cudaStream_t stream)
+{
+    const int32_t rpb = rows_per_block(total_rows, num_sms);
+    const dim3 grid((total_rows + rpb - 1) / rpb, 2);
+    if (f32)
+        cache_write_kernel<float><<<grid, kRowThreads, 0, stream>>>(c, static_cast<const float *>(k),
+                                                                    static_cast<const float *>(v), row_offsets, starts,
+                                                                    total_rows, rpb);
+    else
+        cache_write_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(
+            c, static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v), row_offsets, starts,
+            total_rows, rpb);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(const CacheView &c, bool f32, const int32_t *row_offsets, const int32_t *starts,
+                              int32_t total_rows, void *k, void *v, int num_sms, cudaStream_t stream)
+{
+    const int32_t rpb = rows_per_block(total_rows, num_sms);
+    const dim3 grid((total_rows + rpb - 1) / rpb, 2);
+    if (f32)
+        cache_read_kernel<float><<<grid, kRowThreads, 0, stream>>>(c, row_offsets, starts, total_rows, rpb,
+                                                                   static_cast<float *>(k), static_cast<float *>(v));
+    else
+        cache_read_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(c, row_offsets, starts, total_rows, rpb,
+                                                                           static_cast<__nv_bfloat16 *>(k),
+                                                                           static_cast<__nv_bfloat16 *>(v));
+    return cudaGetLastError();
+}
+
+// One warp per (page, head): its slots are page_size * head_dim consecutive bytes, read 16
+// bytes a lane; each lane sums its sixteen columns over its rows in float32 and the lanes
+// that share columns are added at the end. Pages first, first + 1, ... of a (sequence,
+// head) are dealt to the warps of gridDim.y blocks.
+template <int D>
+__global__ void __launch_bounds__(128)
+    cache_summarize_kernel(const CacheView c, const int32_t *__restrict__ starts, const int32_t *__restrict__ ends,
+                           float *__restrict__ summaries)
+{
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes; // lanes of a row, rows of a load
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t b = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
+    const int32_t first = max(__ldg(starts + b), 0) >> c.page_shift;
+    const int32_t end = max(__ldg(ends + b), 0) >> c.page_shift; // pages below are full
+    if (end > c.max_pages && blockIdx.y == 0 && h == 0 && threadIdx.x == 0) cache_range_error(c);
+    const int32_t stop = min(end, c.max_pages);
+    const int32_t slots = 1 << c.page_shift;
+    const int col = lane % kLanes;
+    for (int32_t pi = first + blockIdx.y * 4 + warp; pi < stop; pi += gridDim.y * 4) {
+        const int32_t id = cache_page(c, b, pi);
+        if (id < 0) {
+            if (lane == 0) cache_range_error(c);
+            continue;
+        }
+        const int64_t row0 = cache_row(c, id, h, 0);
+        const uint4 *src = reinterpret_cast<const uint4 *>(c.k + row0 * D) + lane;
+        const uint8_t *sc = c.k_scales + (row0 + lane / kLanes) * (D / 32) + col / 2;
+        float acc[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+        for (int32_t r = 0; r < slots; r += 2 * kRows) { // page_size is a multiple of 16
+            uint4 w[2];
+            float s[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                w[u] = __ldg(src + (r + u * kRows) * kLanes);
+                s[u] = mx_scale(__ldg(sc + (r + u * kRows) * (D / 32)));
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
+                    acc[2 * i] = fmaf(f.x, s[u], acc[2 * i]);
+                    acc[2 * i + 1] = fmaf(f.y, s[u], acc[2 * i + 1]);
+                }
+            }
+        }
+        const float inv = 1.f / float(slots); // a power of two
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int m = kLanes; m < 32; m <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
+            acc[i] *= inv;
+        }
+        if (lane < kLanes) {
+            float4 *dst = reinterpret_cast<float4 *>(summaries + (int64_t(id) * c.kv_heads + h) * D) + col * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        }
+    }
+}
+
+cudaError_t launch_cache_summarize(const CacheView &c, const int32_t *starts, const int32_t *ends, float *summaries,
+                                   int num_sms, cudaStream_t stream)
+{
+    const int64_t pairs = int64_t(c.batch) * c.kv_heads;
+    int64_t x = (int64_t(num_sms) * 8 + pairs - 1) / pairs, most = (c.max_pages + 3) / 4;
+    if (x > most) x = most;
+    const dim3 grid(unsigned(pairs), unsigned(x < 1 ? 1 : x));
+    if (c.head_dim == 64) cache_summarize_kernel<64><<<grid, 128, 0, stream>>>(c, starts, ends, summaries);
+    else cache_summarize_kernel<128><<<grid, 128, 0, stream>>>(c, starts, ends, summaries);
+    return cudaGetLastError();
+}
+
+namespace {
+
+// Sum over the warp of eight values a lane: three exchange steps that halve the number of
+// values (each lane keeps the half its bit names), then two plain steps. Afterwards lane l
+// holds the total of value 4 b0 + 2 b1 + b2 of its bits (l & 16, l & 8, l & 4).
+__device__ __forceinline__ double reduce8(double (&x)[8], int lane)
+{
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+        const int m = 16 >> s, half = 4 >> s;
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const double give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+        }
+    }
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+    return x[0];
+}
+
+// A score as a 64-bit number that orders like it; NaN below every number, and 0 is left for
+// pages that are no candidates.
+__device__ __forceinline__ uint64_t score_key(double s)
+{
+    if (s != s) return 1;
+    const uint64_t b = uint64_t(__double_as_longlong(s + 0.0)); // -0 becomes +0
+    return (b >> 63) ? ~b : b | (uint64_t(1) << 63);
+}
+
+} // namespace
+
+// Scores of the candidate pages for kRows rows of one (sequence, key/value head), then the
+// topk of each. Scores are formed in float64: the products of bf16 queries and float32 means
+// are exact there and the sums are off by some 2^-53, so that which of two pages wins does
+// not hang on the order of summation (in float32 some 1 in 10^4 rows would choose another
+// page at its last place). kRows = 1 takes eight pages at a time, kRows = 8 one page for
+// eight rows (each mean read and widened once for them); either way a lane has eight
+// partial sums of D / 32 columns to reduce.
+// The topk-th largest key is found bit by bit from the keys' highest differing bit down:
+// each step counts the keys at or above a trial value. Ties go to the lowest page.
+template <int D, int kRows>
+__global__ void __launch_bounds__(256)
+    cache_select_kernel(const CacheView c, const CacheQuery q, const float *__restrict__ summaries, int32_t topk,
+                        uint32_t *__restrict__ page_mask)
+{
+    constexpr int C = D / 32;                     // columns a lane holds
+    constexpr int kPages = 8 / kRows;             // pages a warp takes at once
+    extern __shared__ uint64_t keys[];            // [kRows][max_pages]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t h = blockIdx.y;
+    // the sequence and its tile of kRows rows: tiles are numbered floor(offs[b] / kRows) + b on
+    int32_t b, tile;
+    {
+        int32_t lo = 0, n = c.batch;
+        while (n > 1) {
+            const int32_t step = (n + 31) / 32, at = lo + lane * step;
+            const bool ok = lane * step < n && __ldg(q.q_offsets + at) / kRows + at <= int32_t(blockIdx.x);
+            const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
+            n = min(step, n - (cnt - 1) * step);
+            lo += (cnt - 1) * step;
+        }
+        b = lo;
+        tile = int32_t(blockIdx.x) - (__ldg(q.q_offsets + b) / kRows + b);
+    }
+    const int32_t q0 = __ldg(q.q_offsets + b), n = __ldg(q.q_offsets + b + 1) - q0;
+    const int32_t t0 = tile * kRows;
+    if (t0 >= n) return;
+    const int32_t len = max(__ldg(q.lens + b), 0);
+    const int32_t full = min(len >> c.page_shift, c.max_pages); // pages below are full
+    // candidates of row t: pages that start before its window and are full
+    int32_t cand[kRows], most = 0;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        cand[r] = 0;
+        if (t0 + r < n) {
+            const int32_t pos = query_position(q, q0, len, t0 + r);
+            const int32_t ws = pos >= 0 ? rule_start(q, pos) : 0;
+            const int32_t before = int32_t((int64_t(ws) + (1 << c.page_shift) - 1) >> c.page_shift);
+            cand[r] = min(before, full);
+        }
+        most = max(most, cand[r]);
+    }
+    // this lane's columns of the rows' query sums over the group
+    double qs[kRows][C];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) qs[r][i] = 0.0;
+        if (t0 + r < n) {
+            const __nv_bfloat16 *src =
+                q.q + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * q.group * D + lane * C;
+            for (int32_t g = 0; g < q.group; ++g, src += D) {
+#pragma unroll
+                for (int i = 0; i < C; i += 2) {
+                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(src + i));
+                    qs[r][i] += double(f.x);
+                    qs[r][i + 1] += double(f.y);
+                }
+            }
+        }
+    }
+    for (int32_t p0 = warp * 32; p0 < most; p0 += 8 * 32) {
+        int32_t id = 0;
+        if (p0 + lane < most) {
+            id = cache_page(c, b, p0 + lane);
+            if (id < 0) cache_range_error(c);
+        }
+        const int32_t here = min(32, most - p0);
+        for (int32_t j = 0; j < here; j += kPages) {
+            float f[kPages][C];
+            int32_t ids[kPages];
+#pragma unroll
+            for (int u = 0; u < kPages; ++u) {
+                ids[u] = __shfl_sync(0xffffffffu, id, (j + u) & 31);
+                const float *src = summaries + (int64_t(max(ids[u], 0)) * c.kv_heads + h) * D + lane * C;
+                const bool in = j + u < here;
+                if constexpr (C == 4) {
+                    const float4 x = in ? __ldg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
+                    f[u][0] = x.x, f[u][1] = x.y, f[u][2] = x.z, f[u][3] = x.w;
+                } else {
+                    const float2 x = in ? __ldg(reinterpret_cast<const float2 *>(src)) : make_float2(0, 0);
+                    f[u][0] = x.x, f[u][1] = x.y;
+                }
+            }
+            double part[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int u = kRows == 1 ? i : 0, r = kRows == 1 ? 0 : i;
+                part[i] = 0.0;
+#pragma unroll
+                for (int x = 0; x < C; ++x) part[i] = fma(qs[r][x], double(f[u][x]), part[i]);
+            }
+            const double s = reduce8(part, lane);
+            if ((lane & 3) == 0) {
+                const int i = ((lane & 16) ? 4 : 0) + ((lane & 8) ? 2 : 0) + ((lane & 4) ? 1 : 0);
+                const int u = kRows == 1 ? i : 0, r = kRows == 1 ? 0 : i;
+                int32_t idu = ids[0], cr = cand[0];
+#pragma unroll
+                for (int x = 1; x < kPages; ++x)
+                    if (u == x) idu = ids[x];
+#pragma unroll
+                for (int x = 1; x < kRows; ++x)
+                    if (r == x) cr = cand[x];
+                const int32_t page = p0 + j + u;
+                if (j + u < here)
+                    keys[int64_t(r) * c.max_pages + page] = page < cr && idu >= 0 ? score_key(s) : 0;
+            }
+        }
+    }
+    __syncthreads();
+    const int32_t words = (c.max_pages + 31) / 32;
+    for (int32_t r = warp; r < kRows && t0 + r < n; r += 8) {
+        const uint64_t *key = keys + int64_t(r) * c.max_pages;
+        uint32_t *dst = page_mask + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * words;
+        // range of the keys and number of candidates
+        uint64_t top = 0, low = ~uint64_t(0);
+        int32_t live = 0;
+        for (int32_t p = lane; p < most; p += 32) {
+            const uint64_t x = key[p];
+            if (x) {
+                top = max(top, x);
+                low = min(low, x);
+                ++live;
+            }
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) {
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+            low = min(low, __shfl_xor_sync(0xffffffffu, low, m));
+        }
+        live = __reduce_add_sync(0xffffffffu, live);
+        uint64_t edge = 1;      // keys above it are taken,
+        int32_t equal = 0;      // and this many of those equal to it
+        if (live > topk) {
+            // the largest edge with at least topk keys at or above it
+            int bit = 63 - __clzll(top ^ low);                          // -1: all alike
+            edge = bit < 0 ? top : top & ~((uint64_t(2) << bit) - 1);   // the common prefix
+            int32_t count = live;
+            for (; bit >= 0 && count != topk; --bit) {
+                const uint64_t trial = edge | (uint64_t(1) << bit);
+                int32_t cnt = 0;
+                for (int32_t p = lane; p < most; p += 32) cnt += key[p] >= trial;
+                cnt = __reduce_add_sync(0xffffffffu, cnt);
+                if (cnt >= topk) {
+                    edge = trial;
+                    count = cnt;
+                }
+            }
+            int32_t above = 0;
+            for (int32_t p = lane; p < most; p += 32) above += key[p] > edge;
+            equal = topk - __reduce_add_sync(0xffffffffu, above);
+            if (count == topk) equal = topk; // every key at or above the edge
+        } else {
+            equal = topk;
+        }
+        int32_t seen = 0;
+        for (int32_t w = 0; w < words; ++w) {
+            const int32_t p = w * 32 + lane;
+            const uint64_t x = p < most ? key[p] : 0;
+            const bool even = x == edge && x != 0;
+            const uint32_t ties = __ballot_sync(0xffffffffu, even);
+            const int32_t rank = seen + __popc(ties & ((1u << lane) - 1));
+            const bool take = x > edge || (even && rank < equal);
+            seen += __popc(ties);
+            const uint32_t word = __ballot_sync(0xffffffffu, take);
+            if (lane == 0) dst[w] = word;
+        }
+    }
+}
+
+namespace {
+
+template <int D, int kRows>
+cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *summaries, int32_t topk,
+                          uint32_t *page_mask, cudaStream_t stream)
+{
+    auto kern = cache_select_kernel<D, kRows>;
+    const size_t smem = size_t(kRows) * c.max_pages * 8;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(q.rows / kRows + c.batch, c.kv_heads);
+    kern<<<grid, 256, smem, stream>>>(c, q, summaries, topk, page_mask);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_cache_select(const CacheView &c, const CacheQuery &q, const float *summaries, int32_t topk,
+                                uint32_t *page_mask, int, cudaStream_t stream)
+{
+    // eight rows a block read each mean once; single events, and rows whose eight key arrays
+    // would not fit in shared memory, go one row a block
+    const bool eight = int64_t(q.rows) > 2 * int64_t(c.batch) && c.max_pages <= kSelectMaxPages / 8;
+    if (c.head_dim == 64)
+        return eight ? launch_select<64, 8>(c, q, summaries, topk, page_mask, stream)
+                     : launch_select<64, 1>(c, q, summaries, topk, page_mask, stream);
+    return eight ? launch_select<128, 8>(c, q, summaries, topk, page_mask, stream)
+                 : launch_select<128, 1>(c, q, summaries, topk, page_mask, stream);
+}
+
+} // namespace ba

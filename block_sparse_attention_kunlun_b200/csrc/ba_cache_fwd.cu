@@ -1,0 +1,436 @@
+// Attention of new queries over a history cache (single events, chunks, trees of drafted
+// events, candidates): block attention's serving form.
+//
+// Query row t of sequence b (position pos, first position its window shows ws, by the block
+// rule of ba_common.cuh) sees
+//   cached slot p < len        <=>  p <= pos and (p >= ws or the bit of p's page is set)
+//   drafted row j (slot len+j) <=>  its tree bit is set (no tree: j <= t) and ws <= pos_j <= pos
+// and out = softmax(q k / sqrt(D)) v over what it sees, lse the log of the normaliser. A row
+// that sees nothing gets out = 0, lse = -inf.
+//
+// A block takes one tile of query rows (tokens times the heads that share a key/value head)
+// and one stretch of slots (a split); with several splits the blocks leave their running
+// maximum, sum and unnormalised output in float32 and cache_combine_kernel joins them in the
+// order of the splits. Blocks find their sequence themselves: tiles are numbered
+// floor(offs[b] * group / tile_rows) + b, which leaves at least ceil(rows / tile_rows) numbers
+// for every sequence, so no pass over the batch comes first.
+#include "ba_cache.cuh"
+#include "ba_kernels.cuh"
+#include "ba_ptx.cuh"
+
+namespace ba {
+
+namespace {
+
+// One block's work.
+struct FwdTile {
+    int32_t b, q0, n;       // sequence, its first row, its rows
+    int32_t len;            // cached slots
+    int32_t row0, rows;     // first row (token * group + head) of the tile, valid rows
+    int32_t end;            // slots at and past it are empty
+};
+
+// Tile number blockIdx.x of `tile_rows` rows; false: the number is unused. Warp-collective.
+__device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, FwdTile &t)
+{
+    const int lane = threadIdx.x & 31;
+    const int32_t *offs = p.q.q_offsets;
+    int32_t lo = 0, n = p.c.batch;
+    while (n > 1) {
+        const int32_t step = (n + 31) / 32, at = lo + lane * step;
+        const bool ok =
+            lane * step < n && int64_t(__ldg(offs + at)) * p.q.group / tile_rows + at <= int64_t(blockIdx.x);
+        const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
+        n = min(step, n - (cnt - 1) * step);
+        lo += (cnt - 1) * step;
+    }
+    t.b = lo;
+    t.q0 = __ldg(offs + lo);
+    t.n = __ldg(offs + lo + 1) - t.q0;
+    const int64_t first = int64_t(t.q0) * p.q.group / tile_rows + lo;
+    const int64_t row0 = (int64_t(blockIdx.x) - first) * tile_rows, all = int64_t(t.n) * p.q.group;
+    if (row0 >= all) return false;
+    t.row0 = int32_t(row0);
+    t.rows = int32_t(min(all - row0, int64_t(tile_rows)));
+    const int64_t cap = int64_t(p.c.max_pages) << p.c.page_shift;
+    const int64_t len = max(__ldg(p.q.lens + lo), 0);
+    if (len + t.n > cap && threadIdx.x == 0) cache_range_error(p.c);
+    t.len = int32_t(min(len, cap));
+    t.end = int32_t(min(len + t.n, cap));
+    return true;
+}
+
+// One query row's view of the slots.
+struct RowView {
+    int32_t tok, pos, ws; // token within the sequence; nothing is visible for pos < 0
+};
+
+__device__ __forceinline__ RowView row_view(const CacheFwd &p, const FwdTile &t, int32_t row)
+{
+    RowView r;
+    r.tok = row / p.q.group;
+    r.pos = query_position(p.q, t.q0, t.len, r.tok);
+    r.ws = r.pos >= 0 ? rule_start(p.q, r.pos) : 0;
+    return r;
+}
+
+// Whether row r sees slot s (s < t.end).
+__device__ __forceinline__ bool sees(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h, int32_t s)
+{
+    if (s < t.len) {
+        if (s > r.pos) return false;
+        if (s >= r.ws) return true;
+        if (!p.page_mask) return false;
+        const int32_t page = s >> p.c.page_shift;
+        return (__ldg(p.page_mask + ((int64_t(t.q0) + r.tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
+                (page & 31)) & 1u;
+    }
+    const int32_t j = s - t.len;
+    const int32_t pj = query_position(p.q, t.q0, t.len, j);
+    if (pj > r.pos || pj < r.ws) return false;
+    if (!p.tree) return j <= r.tok;
+    return (j >> 5) < p.tree_words &&
+           ((__ldg(p.tree + (int64_t(t.q0) + r.tok) * p.tree_words + (j >> 5)) >> (j & 31)) & 1u);
+}
+
+constexpr int kSimtWarps = 4;
+constexpr int kGroup = 16; // consecutive aligned slots, always of one page
+
+} // namespace
+
+// A few query rows (kR) of one key/value head, on the CUDA cores: with one to four rows a
+// key, the bytes of the cache are the bound and a tensor-core tile would be all but empty.
+// A warp reads 16 slots of keys and of values, each a contiguous piece of its page, 16 bytes
+// (16 codes) a lane: D / 16 lanes hold a slot. They are widened to float32 in registers, a
+// score is a 16-term dot product in each lane and three (two) shuffles, and the value's lane
+// adds its 16 columns into its own running sum: each set of D / 16 lanes keeps the running
+// maximum and sum of the slots it has met, so the softmax needs no exchange inside the loop.
+// The sets and the warps are joined once at the end.
+template <int D, int kR>
+__global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const CacheFwd p)
+{
+    constexpr int kLanes = D / 16;      // lanes of a slot
+    constexpr int kSets = 32 / kLanes;  // slots of a load
+    constexpr int kU = kGroup / kSets;  // loads of a group
+    __shared__ float sm_o[kSimtWarps][kR][D];
+    __shared__ float2 sm_ml[kSimtWarps][kR];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t h = blockIdx.y, split = blockIdx.z;
+    FwdTile t;
+    if (!find_tile(p, kR, t)) return;
+    const int col = lane % kLanes, set = lane / kLanes;
+    RowView rv[kR];
+    float2 q[kR][8];
+    int32_t min_ws = INT32_MAX, max_ws = 0, min_pos = INT32_MAX, max_pos = -1;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        rv[r] = row_view(p, t, t.row0 + min(r, t.rows - 1));
+        min_ws = min(min_ws, rv[r].ws);
+        max_ws = max(max_ws, rv[r].ws);
+        min_pos = min(min_pos, rv[r].pos);
+        max_pos = max(max_pos, rv[r].pos);
+        const int32_t row = t.row0 + min(r, t.rows - 1);
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            p.q.q + ((int64_t(t.q0) + rv[r].tok) * p.c.kv_heads * p.q.group + h * p.q.group + row % p.q.group) * D +
+            col * 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 w = __ldg(src + i);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                q[r][4 * i + x] = make_float2(__uint_as_float(ws[x] << 16) * p.scale_log2,
+                                              __uint_as_float(ws[x] & 0xffff0000u) * p.scale_log2);
+        }
+    }
+    // this split's slots, in groups of 16
+    const int32_t lo = (p.page_mask ? 0 : min_ws) / kGroup * kGroup;
+    int64_t from = lo + int64_t(split) * p.chunk, to = split + 1 == p.nsplit ? t.end : from + p.chunk;
+    if (to > t.end) to = t.end;
+    // `from` is a multiple of 16; a split that starts past the end has nothing
+    const int32_t g1 = int32_t((to + kGroup - 1) / kGroup), g0 = from < t.end ? int32_t(from / kGroup) : g1;
+
+    float m[kR], l[kR];
+    float2 o[kR][8];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][i] = make_float2(0.f, 0.f);
+    }
+
+    // 16 slots at `slot` on page `id`; vis[r]: the slots that row r sees (kAll: every row all 16)
+    auto take = [&](int32_t slot, int32_t id, auto all_t, const uint32_t *vis) {
+        constexpr bool kAll = decltype(all_t)::value;
+        const int64_t row = cache_row(p.c, id, h, slot & ((1 << p.c.page_shift) - 1));
+        const uint4 *ks = reinterpret_cast<const uint4 *>(p.c.k + row * D) + lane;
+        const uint4 *vs = reinterpret_cast<const uint4 *>(p.c.v + row * D) + lane;
+        const int64_t srow = (row + set) * (D / 32) + col / 2;
+        uint4 kw[kU], vw[kU];
+        uint32_t kc[kU], vc[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            kw[u] = __ldg(ks + u * 32);
+            kc[u] = __ldg(p.c.k_scales + srow + u * kSets * (D / 32));
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            vw[u] = __ldg(vs + u * 32);
+            vc[u] = __ldg(p.c.v_scales + srow + u * kSets * (D / 32));
+        }
+        float s[kR][kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t ws[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
+            float2 acc[kR];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) acc[r] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) acc[r] = ffma2(q[r][i], f, acc[r]);
+            }
+            const float sc = mx_scale(kc[u]);
+#pragma unroll
+            for (int r = 0; r < kR; ++r) s[r][u] = (acc[r].x + acc[r].y) * sc;
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+#pragma unroll
+                for (int x = 1; x < kLanes; x <<= 1) s[r][u] += __shfl_xor_sync(0xffffffffu, s[r][u], x);
+                if (!kAll) s[r][u] = (vis[r] >> (u * kSets + set)) & 1u ? s[r][u] : -INFINITY;
+            }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            float mx = m[r];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) mx = fmaxf(mx, s[r][u]);
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float alpha = ex2_approx(m[r] - ref);
+            m[r] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                s[r][u] = ex2_approx(s[r][u] - ref);
+                sum += s[r][u];
+            }
+            l[r] = fmaf(l[r], alpha, sum);
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[r][i] = fmul2(o[r][i], a2);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t ws[4] = {vw[u].x, vw[u].y, vw[u].z, vw[u].w};
+            const float sc = mx_scale(vc[u]);
+            float2 pr[kR];
+#pragma unroll
+            for (int r = 0; r < kR; ++r) pr[r] = make_float2(s[r][u] * sc, s[r][u] * sc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
+#pragma unroll
+                for (int r = 0; r < kR; ++r) {
+                    // a slot that the row does not see may hold anything (0 * NaN is NaN)
+                    if (kAll) o[r][i] = ffma2(pr[r], f, o[r][i]);
+                    else if ((vis[r] >> (u * kSets + set)) & 1u) o[r][i] = ffma2(pr[r], f, o[r][i]);
+                }
+            }
+        }
+    };
+
+    for (int32_t base = g0; base < g1; base += kSimtWarps * 32) {
+        // 32 groups of this warp: which of them any row may see, and their pages
+        const int32_t g = base + lane * kSimtWarps + warp, slot = g * kGroup;
+        bool want = g < g1 && (slot + kGroup > min_ws || slot + kGroup > t.len);
+        if (g < g1 && !want && p.page_mask) {
+            const int32_t page = slot >> p.c.page_shift;
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+                want |= (__ldg(p.page_mask +
+                               ((int64_t(t.q0) + rv[r].tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
+                         (page & 31)) & 1u;
+        }
+        want = want && (slot <= max_pos || slot + kGroup > t.len);
+        int32_t id = -1;
+        if (want) {
+            id = cache_page(p.c, t.b, slot >> p.c.page_shift);
+            if (id < 0) cache_range_error(p.c);
+        }
+        uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
+        while (todo) {
+            const int x = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int32_t s0 = (base + x * kSimtWarps + warp) * kGroup;
+            const int32_t page = __shfl_sync(0xffffffffu, id, x);
+            if (s0 >= max_ws && s0 + kGroup - 1 <= min(min_pos, t.len - 1)) {
+                take(s0, page, std::true_type{}, nullptr);
+            } else {
+                uint32_t vis[kR];
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+                    vis[r] = __ballot_sync(0xffffffffu, lane < kGroup && s0 + lane < t.end &&
+                                                            sees(p, t, rv[r], h, s0 + lane));
+                take(s0, page, std::false_type{}, vis);
+            }
+        }
+    }
+
+    // join the sets of lanes, then the warps
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+        float mx = m[r];
+#pragma unroll
+        for (int x = kLanes; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float a = ex2_approx(m[r] - (mx == -INFINITY ? 0.f : mx));
+        l[r] *= a;
+#pragma unroll
+        for (int x = kLanes; x < 32; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[r][i].x *= a;
+            o[r][i].y *= a;
+#pragma unroll
+            for (int x = kLanes; x < 32; x <<= 1) {
+                o[r][i].x += __shfl_xor_sync(0xffffffffu, o[r][i].x, x);
+                o[r][i].y += __shfl_xor_sync(0xffffffffu, o[r][i].y, x);
+            }
+        }
+        if (set == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float2 *>(&sm_o[warp][r][col * 16 + 2 * i]) = o[r][i];
+        }
+        if (lane == 0) sm_ml[warp][r] = make_float2(mx, l[r]);
+    }
+    __syncthreads();
+    const int32_t heads = p.c.kv_heads * p.q.group;
+    for (int x = threadIdx.x; x < t.rows * D; x += kSimtWarps * 32) {
+        const int r = x / D, d = x % D;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kSimtWarps; ++w) mx = fmaxf(mx, sm_ml[w][r].x);
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f, acc = 0.f;
+#pragma unroll
+        for (int w = 0; w < kSimtWarps; ++w) {
+            const float a = ex2_approx(sm_ml[w][r].x - ref);
+            sum = fmaf(sm_ml[w][r].y, a, sum);
+            acc = fmaf(sm_o[w][r][d], a, acc);
+        }
+        const int32_t row = t.row0 + r;
+        const int64_t token = int64_t(t.q0) + row / p.q.group;
+        const int32_t head = h * p.q.group + row % p.q.group;
+        const int64_t oh = token * heads + head;
+        if (p.nsplit == 1) {
+            p.out[oh * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+            if (d == 0)
+                p.lse[int64_t(head) * p.q.rows + token] = (mx + log2f(sum)) * 0.6931471805599453f;
+        } else {
+            const int64_t at = int64_t(split) * p.q.rows * heads + oh;
+            p.part_o[at * D + d] = acc;
+            if (d == 0) p.part_ml[at] = make_float2(mx, sum);
+        }
+    }
+}
+
+// Joins the splits of every (row, head): weights 2^(m_s - max m), in the order of the splits.
+// One warp per row and head, D / 32 columns a lane.
+template <int D>
+__global__ void __launch_bounds__(256) cache_combine_kernel(const CacheFwd p)
+{
+    constexpr int C = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int32_t heads = p.c.kv_heads * p.q.group;
+    const int64_t all = int64_t(p.q.rows) * heads, at = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (at >= all) return;
+    float mx = -INFINITY;
+    for (int32_t s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, p.part_ml[s * all + at].x);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = 0.f;
+    for (int32_t s = 0; s < p.nsplit; ++s) {
+        const float2 ml = p.part_ml[s * all + at];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue; // nothing seen there
+        const float a = ex2_approx(ml.x - ref);
+        sum = fmaf(ml.y, a, sum);
+        const float *src = p.part_o + (s * all + at) * D + lane * C;
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] = fmaf(src[i], a, acc[i]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < C; i += 2)
+        *reinterpret_cast<uint32_t *>(p.out + at * D + lane * C + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0) {
+        const int64_t token = at / heads, head = at % heads;
+        p.lse[head * p.q.rows + token] = (mx + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32_t group, int32_t head_dim,
+                            int64_t slots, int64_t block, int64_t window, bool has_mask)
+{
+    CacheFwdPlan plan;
+    const int64_t all = int64_t(rows) * group; // query rows of a key/value head
+    const int64_t each = batch > 0 ? (all + batch - 1) / batch : 1;
+    plan.tile_rows = each <= 1 ? 1 : (each <= 2 ? 2 : 4);
+    plan.tiles = all / plan.tile_rows + batch;
+    // the most slots a tile may meet: the whole cache, or the window and the rows themselves
+    int64_t reach = slots;
+    if (!has_mask) {
+        const int64_t per = batch > 0 ? (int64_t(rows) + batch - 1) / batch : 0;
+        if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
+    }
+    // enough blocks for several on each of the 148 SMs, of no fewer than 256 slots
+    const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
+    const int64_t items = (work > batch ? work : batch) * kv_heads;
+    int64_t n = (148 * 10 + items - 1) / (items > 0 ? items : 1);
+    const int64_t most = (reach + 255) / 256;
+    if (n > most) n = most;
+    if (n < 1) n = 1;
+    plan.chunk = int32_t(((reach + n - 1) / n + 15) / 16 * 16);
+    plan.nsplit = int32_t((reach + plan.chunk - 1) / plan.chunk);
+    if (plan.nsplit < 1) plan.nsplit = 1;
+    const size_t parts = plan.nsplit > 1 ? size_t(plan.nsplit) * size_t(all) * kv_heads : 0;
+    plan.bytes = align256(parts * 8) + align256(parts * head_dim * 4);
+    return plan;
+}
+
+namespace {
+
+template <int D, int kR>
+void launch_simt(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
+{
+    const dim3 grid(unsigned(plan.tiles), unsigned(p.c.kv_heads), unsigned(p.nsplit));
+    cache_fwd_simt_kernel<D, kR><<<grid, kSimtWarps * 32, 0, stream>>>(p);
+}
+
+template <int D>
+cudaError_t launch_d(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
+{
+    if (plan.tile_rows == 1) launch_simt<D, 1>(p, plan, stream);
+    else if (plan.tile_rows == 2) launch_simt<D, 2>(p, plan, stream);
+    else launch_simt<D, 4>(p, plan, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.nsplit == 1) return e;
+    const int64_t rows = int64_t(p.q.rows) * p.c.kv_heads * p.q.group;
+    cache_combine_kernel<D><<<unsigned((rows + 7) / 8), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_cache_fwd(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
+{
+    return p.c.head_dim == 64 ? launch_d<64>(p, plan, stream) : launch_d<128>(p, plan, stream);
+}
+
+} // namespace ba

@@ -358,13 +358,142 @@ ba_status ba_fwd_noalloc(const ba_problem *p, const void *q, const void *k, cons
                          const uint8_t *skip, void *out, float *lse, ba_stream_t stream);
 
 /*
+ * A history cache, for serving (the pages describe training; that a served
+ * history grows event by event, and that drafted or candidate events look at
+ * it, is this library's reading). Keys and values of every history live in
+ * pages, quantised as they are written (MXFP8, the format above: E4M3
+ * elements, one E8M0 scale for 32 of them along head_dim), so that one slot
+ * takes 2 * (head_dim + head_dim / 32) bytes a head, 0.52 of bf16.
+ *
+ *  - k, v: DEVICE bytes [num_pages, kv_heads, page_size, head_dim];
+ *    k_scales, v_scales: DEVICE bytes [num_pages, kv_heads, page_size,
+ *    head_dim / 32]; all 16-byte aligned.
+ *  - page_table: DEVICE int32 [batch, max_pages]. Slot p of sequence b, the
+ *    event at position p of its history, is row p % page_size of page
+ *    page_table[b * max_pages + p / page_size]. Entries outside
+ *    [0, num_pages) mean "no page". Sequences may share pages that are only
+ *    read; two calls, or two sequences of one call, must not write a page
+ *    that the other reads or writes at the same time.
+ *  - status: DEVICE int32 word or NULL. The calls only ever set bits in it;
+ *    the caller zeroes it. After a call met a slot past max_pages or without
+ *    a page (skipped: nothing outside the pools is read or written),
+ *    ba_device_status(status, stream) returns BA_ERR_INVALID_ARG.
+ *  - page_size 16, 32, 64 or 128; head_dim 64 or 128 (else
+ *    BA_ERR_UNSUPPORTED); kv_heads <= 65535; max_pages * page_size < 2^31.
+ *
+ * The calls take lengths and starts as DEVICE arrays, so they can be captured
+ * into a graph and replayed while the histories grow.
+ */
+typedef struct {
+    void *k, *v;
+    void *k_scales, *v_scales;
+    const int32_t *page_table;
+    int32_t *status;
+    int32_t batch, max_pages, num_pages, page_size, kv_heads, head_dim;
+} ba_cache;
+
+/*
+ * ba_cache_write: row t of sequence b of the dense, jagged k and v (rows
+ * row_offsets[b] .. row_offsets[b+1]-1 of DEVICE [total_rows, kv_heads,
+ * head_dim] tensors, float32 or bf16) is quantised into slot starts[b] + t.
+ * Scale and elements as ba_mx_quantize's. A NaN does not count for its
+ * block's scale and becomes E4M3's NaN; an infinity sets the scale to 2^120
+ * and becomes the largest code (448). Rows whose slot is negative, past
+ * max_pages or without a page are skipped, and the status word says so.
+ *
+ * ba_cache_read: the reverse: row t of sequence b of k and v receives slot
+ * starts[b] + t as element * 2^e, rounded to the nearest bf16 (exact unless
+ * subnormal) or exact in float32. A slot that does not exist gives zeros
+ * and sets the status word.
+ *
+ * row_offsets: DEVICE int32 [batch + 1], row_offsets[0] = 0, non-decreasing,
+ * row_offsets[batch] = total_rows (not checked on the device); starts: DEVICE
+ * int32 [batch].
+ */
+ba_status ba_cache_write(const ba_cache *cache, ba_dtype dtype, const void *k, const void *v,
+                         const int32_t *row_offsets, const int32_t *starts, int32_t total_rows, ba_stream_t stream);
+ba_status ba_cache_read(const ba_cache *cache, ba_dtype dtype, const int32_t *row_offsets, const int32_t *starts,
+                        int32_t total_rows, void *k, void *v, ba_stream_t stream);
+
+/*
+ * ba_cache_summarize: the mean key of every page of sequence b that has at
+ * least one slot in [starts[b], ends[b]) and is full at ends[b] (all its
+ * slots lie below ends[b]): summaries[page][head] = sum of the page's
+ * page_size dequantised keys / page_size. summaries: DEVICE float32
+ * [num_pages, kv_heads, head_dim], 16-byte aligned, indexed by page number;
+ * other pages' entries are left as they are. Call it after ba_cache_write
+ * with the slots that were written.
+ */
+ba_status ba_cache_summarize(const ba_cache *cache, const int32_t *starts, const int32_t *ends, float *summaries,
+                             ba_stream_t stream);
+
+/*
+ * ba_cache_select: which pages outside its window a query should look at.
+ * The problem describes the queries: q DEVICE bf16 [total_tokens, heads,
+ * head_dim], heads a multiple of the cache's kv_heads (query head x uses
+ * key/value head x / (heads / kv_heads)), batch and head_dim the cache's;
+ * sequence b owns rows q_offsets[b] .. q_offsets[b+1]-1. lens: DEVICE int32
+ * [batch], the cached slots of each sequence. positions: DEVICE int32
+ * [total_tokens], each query's position in its history, or NULL for
+ * lens[b] + t (row t of sequence b).
+ *
+ * Let ws be the first position that the block rule shows to a query. Page c
+ * of its sequence is a candidate when it starts before ws and is full
+ * ((c + 1) * page_size <= lens[b]). Its score for key/value head h is
+ *     sum over the heads x of h's group of q_x . summaries[page][h],
+ * formed in float64. The topk candidates with the largest scores are
+ * selected (all of them when there are fewer), ties to the lower page, NaN
+ * below every number. page_mask: DEVICE uint32 [total_tokens, kv_heads,
+ * ceil(max_pages / 32)]: bit c % 32 of word c / 32 is set for a selected
+ * page c; every word is written. max_pages <= 16384 (else
+ * BA_ERR_UNSUPPORTED); topk >= 1.
+ */
+ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, const void *q, const int32_t *q_offsets,
+                          const int32_t *lens, const int32_t *positions, const float *summaries, int32_t block,
+                          int32_t window, int32_t topk, uint32_t *page_mask, ba_stream_t stream);
+
+/*
+ * ba_cache_fwd: attention of new events over the cache: one event a
+ * sequence, a chunk of them, a tree of drafted events or a set of candidates.
+ * Their keys and values have been written to slots lens[b] + t (row t of
+ * sequence b) by ba_cache_write; lens counts the slots before them.
+ * Arguments as ba_cache_select's. With pos the position of query row t and
+ * ws the first position that the block rule shows to it, the row sees
+ *   - cached slot p < lens[b]  <=>  p <= pos, and p >= ws or page_mask has
+ *     the bit of p's page (page_mask NULL: no page is selected);
+ *   - row j of its own sequence, itself included  <=>
+ *     ws <= position of row j <= pos, and bit j of tree_mask's row t is set
+ *     (tree_mask NULL: j <= t).
+ * tree_mask: DEVICE uint32 [total_tokens, tree_words], bit j % 32 of word
+ * j / 32 for row j of the same sequence; rows past tree_words * 32 are not
+ * seen. A row without tree_mask and positions is what ba_fwd computes for the
+ * event at that position, on the dequantised keys and values, and so is each
+ * row of a tree for the history that ends in its path. out: DEVICE bf16 like
+ * q; lse: DEVICE float32 [heads, total_tokens]. A row that sees nothing
+ * gets out = 0 and lse = -infinity; what a row does not see, NaN and
+ * infinity included, does not reach it. Queries at negative positions see
+ * nothing.
+ *
+ * BF16 only; head_dim 64 or 128. Workspace: ba_cache_fwd_workspace_size
+ * bytes, enough with and without page_mask (it may be 0, and workspace
+ * NULL); it depends on the sizes in the two structs, block and window, not
+ * on the lengths. Results do not depend on timing or on earlier calls.
+ */
+size_t ba_cache_fwd_workspace_size(const ba_cache *cache, const ba_problem *problem, int32_t block, int32_t window);
+ba_status ba_cache_fwd(const ba_cache *cache, const ba_problem *problem, const void *q, const int32_t *q_offsets,
+                       const int32_t *lens, const int32_t *positions, const uint32_t *tree_mask, int32_t tree_words,
+                       const uint32_t *page_mask, int32_t block, int32_t window, void *out, float *lse,
+                       void *workspace, size_t workspace_bytes, ba_stream_t stream);
+
+/*
  * Waits for `stream`, then reads the status word that previous calls (ba_fwd,
  * ba_bwd and the other entry points) left in `workspace`. Returns:
  *  - BA_OK;
  *  - BA_ERR_TIMEOUT if a kernel gave up waiting (its outputs are then
  *    undefined);
  *  - BA_ERR_INVALID_ARG if a rotary call met an example longer than its
- *    tables;
+ *    tables, or (given a cache's status word) a cache call met a slot
+ *    outside the cache;
  *  - BA_ERR_CUDA if the read itself failed.
  */
 ba_status ba_device_status(const void *workspace, ba_stream_t stream);
@@ -417,7 +546,8 @@ ba_status ba_selftest_activation(ba_activation act, const float *x, float *y, fl
  * Profiling hook. Until changed, calls made from THIS host thread record
  * `start` on their stream right before one kernel and `stop` right after it,
  * so that cudaEventElapsedTime(start, stop) is that kernel's own duration:
- * which = 0 the forward attention kernel of ba_fwd (or ba_gdpa_fwd), 1 the
+ * which = 0 the forward attention kernel of ba_fwd (or ba_gdpa_fwd; all of
+ * ba_cache_fwd's kernels), 1 the
  * dQ kernel of ba_bwd (ba_gdpa_bwd), 2 its dK/dV kernel. The events are cudaEvent_t handles owned by
  * the caller; pass NULL, NULL to stop recording. Returns BA_ERR_INVALID_ARG
  * for another `which`. Only the hook pointers are stored (thread-local);
