@@ -833,8 +833,9 @@ ba_status check_cache(const ba_cache *c, CacheView &view)
     if (c->head_dim != 64 && c->head_dim != 128) return BA_ERR_UNSUPPORTED;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return BA_ERR_UNSUPPORTED;
-    // slots are numbered in 31 bits, heads are a grid dimension, (sequence, head) pairs too
-    if (int64_t(c->max_pages) * c->page_size > INT32_MAX || c->kv_heads > 65535 ||
+    // slots, and tiles of them past the end, are numbered in 31 bits; heads are a grid dimension,
+    // (sequence, head) pairs too
+    if (int64_t(c->max_pages) * c->page_size > (1 << 30) || c->kv_heads > 65535 ||
         int64_t(c->batch) * c->kv_heads > INT32_MAX)
         return BA_ERR_UNSUPPORTED;
     int shift = 4;
@@ -884,7 +885,7 @@ ba_status need_b200(int &num_sms)
 CacheFwdPlan plan_for(const ba_cache &c, const ba_problem &p, int32_t block, int32_t window, bool has_mask)
 {
     return cache_fwd_plan(p.batch, p.total_tokens, c.kv_heads, p.heads / c.kv_heads, p.head_dim,
-                          int64_t(c.max_pages) * c.page_size, block, window, has_mask);
+                          int64_t(c.max_pages) * c.page_size, c.page_size, block, window, has_mask);
 }
 
 } // namespace
@@ -974,6 +975,7 @@ ba_status ba_cache_fwd(const ba_cache *cache, const ba_problem *problem, const v
     if (st != BA_OK || (st = check_queries(*cache, problem, block, window)) != BA_OK) return st;
     const ba_problem &P = *problem;
     if (tree_words < 0 || (tree_mask && tree_words < 1)) return BA_ERR_INVALID_ARG;
+    if (page_mask && f.c.max_pages > kSelectMaxPages) return BA_ERR_UNSUPPORTED;
     if (P.total_tokens == 0) return BA_OK;
     if (!q || !aligned(q, 16) || !q_offsets || !aligned(q_offsets, 4) || !lens || !aligned(lens, 4) ||
         !aligned(positions, 4) || !aligned(tree_mask, 4) || !aligned(page_mask, 4) || !out || !aligned(out, 16) ||

@@ -133,7 +133,8 @@ struct CacheFwdPlan {
     size_t bytes;
 };
 CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32_t group, int32_t head_dim,
-                            int64_t slots, int64_t block, int64_t window, bool has_mask);
+                            int64_t slots, int32_t page_size, int64_t block, int64_t window,
+                            bool has_mask);
 cudaError_t launch_cache_fwd(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream);
 
 } // namespace ba

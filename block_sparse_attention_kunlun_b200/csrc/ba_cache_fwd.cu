@@ -14,84 +14,13 @@
 // order of the splits. Blocks find their sequence themselves: tiles are numbered
 // floor(offs[b] * group / tile_rows) + b, which leaves at least ceil(rows / tile_rows) numbers
 // for every sequence, so no pass over the batch comes first.
-#include "ba_cache.cuh"
+#include "ba_cache_fwd.cuh"
 #include "ba_kernels.cuh"
 #include "ba_ptx.cuh"
 
 namespace ba {
 
 namespace {
-
-// One block's work.
-struct FwdTile {
-    int32_t b, q0, n;       // sequence, its first row, its rows
-    int32_t len;            // cached slots
-    int32_t row0, rows;     // first row (token * group + head) of the tile, valid rows
-    int32_t end;            // slots at and past it are empty
-};
-
-// Tile number blockIdx.x of `tile_rows` rows; false: the number is unused. Warp-collective.
-__device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, FwdTile &t)
-{
-    const int lane = threadIdx.x & 31;
-    const int32_t *offs = p.q.q_offsets;
-    int32_t lo = 0, n = p.c.batch;
-    while (n > 1) {
-        const int32_t step = (n + 31) / 32, at = lo + lane * step;
-        const bool ok =
-            lane * step < n && int64_t(__ldg(offs + at)) * p.q.group / tile_rows + at <= int64_t(blockIdx.x);
-        const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
-        n = min(step, n - (cnt - 1) * step);
-        lo += (cnt - 1) * step;
-    }
-    t.b = lo;
-    t.q0 = __ldg(offs + lo);
-    t.n = __ldg(offs + lo + 1) - t.q0;
-    const int64_t first = int64_t(t.q0) * p.q.group / tile_rows + lo;
-    const int64_t row0 = (int64_t(blockIdx.x) - first) * tile_rows, all = int64_t(t.n) * p.q.group;
-    if (row0 >= all) return false;
-    t.row0 = int32_t(row0);
-    t.rows = int32_t(min(all - row0, int64_t(tile_rows)));
-    const int64_t cap = int64_t(p.c.max_pages) << p.c.page_shift;
-    const int64_t len = max(__ldg(p.q.lens + lo), 0);
-    if (len + t.n > cap && threadIdx.x == 0) cache_range_error(p.c);
-    t.len = int32_t(min(len, cap));
-    t.end = int32_t(min(len + t.n, cap));
-    return true;
-}
-
-// One query row's view of the slots.
-struct RowView {
-    int32_t tok, pos, ws; // token within the sequence; nothing is visible for pos < 0
-};
-
-__device__ __forceinline__ RowView row_view(const CacheFwd &p, const FwdTile &t, int32_t row)
-{
-    RowView r;
-    r.tok = row / p.q.group;
-    r.pos = query_position(p.q, t.q0, t.len, r.tok);
-    r.ws = r.pos >= 0 ? rule_start(p.q, r.pos) : 0;
-    return r;
-}
-
-// Whether row r sees slot s (s < t.end).
-__device__ __forceinline__ bool sees(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h, int32_t s)
-{
-    if (s < t.len) {
-        if (s > r.pos) return false;
-        if (s >= r.ws) return true;
-        if (!p.page_mask) return false;
-        const int32_t page = s >> p.c.page_shift;
-        return (__ldg(p.page_mask + ((int64_t(t.q0) + r.tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
-                (page & 31)) & 1u;
-    }
-    const int32_t j = s - t.len;
-    const int32_t pj = query_position(p.q, t.q0, t.len, j);
-    if (pj > r.pos || pj < r.ws) return false;
-    if (!p.tree) return j <= r.tok;
-    return (j >> 5) < p.tree_words &&
-           ((__ldg(p.tree + (int64_t(t.q0) + r.tok) * p.tree_words + (j >> 5)) >> (j & 31)) & 1u);
-}
 
 constexpr int kSimtWarps = 4;
 constexpr int kGroup = 16; // consecutive aligned slots, always of one page
@@ -376,12 +305,14 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const CacheFwd p)
 }
 
 CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32_t group, int32_t head_dim,
-                            int64_t slots, int64_t block, int64_t window, bool has_mask)
+                            int64_t slots, int32_t page_size, int64_t block, int64_t window,
+                            bool has_mask)
 {
     CacheFwdPlan plan;
     const int64_t all = int64_t(rows) * group; // query rows of a key/value head
     const int64_t each = batch > 0 ? (all + batch - 1) / batch : 1;
-    plan.tile_rows = each <= 1 ? 1 : (each <= 2 ? 2 : 4);
+    plan.tile_rows = each <= 1 ? 1 : (each <= 2 ? 2 : (each <= 4 ? 4 : kMmaRows));
+    const bool mma = plan.tile_rows == kMmaRows;
     plan.tiles = all / plan.tile_rows + batch;
     // the most slots a tile may meet: the whole cache, or the window and the rows themselves
     int64_t reach = slots;
@@ -392,12 +323,17 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     // enough blocks for several on each of the 148 SMs, of no fewer than 256 slots
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
     const int64_t items = (work > batch ? work : batch) * kv_heads;
-    int64_t n = (148 * 10 + items - 1) / (items > 0 ? items : 1);
+    int64_t n = (148 * (mma ? 6 : 10) + items - 1) / (items > 0 ? items : 1);
     const int64_t most = (reach + 255) / 256;
     if (n > most) n = most;
     if (n < 1) n = 1;
-    plan.chunk = int32_t(((reach + n - 1) / n + 15) / 16 * 16);
-    plan.nsplit = int32_t((reach + plan.chunk - 1) / plan.chunk);
+    int64_t chunk = ((reach + n - 1) / n + 63) / 64 * 64;
+    if (mma && has_mask) {
+        const int64_t unit = page_size < 64 ? page_size : 64;
+        if (chunk > kMmaList * unit) chunk = kMmaList * unit;
+    }
+    plan.chunk = int32_t(chunk);
+    plan.nsplit = int32_t((reach + chunk - 1) / chunk);
     if (plan.nsplit < 1) plan.nsplit = 1;
     const size_t parts = plan.nsplit > 1 ? size_t(plan.nsplit) * size_t(all) * kv_heads : 0;
     plan.bytes = align256(parts * 8) + align256(parts * head_dim * 4);
@@ -416,7 +352,10 @@ void launch_simt(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t strea
 template <int D>
 cudaError_t launch_d(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
 {
-    if (plan.tile_rows == 1) launch_simt<D, 1>(p, plan, stream);
+    if (plan.tile_rows == kMmaRows) {
+        const cudaError_t e = launch_cache_fwd_mma<D>(p, plan, stream);
+        if (e != cudaSuccess) return e;
+    } else if (plan.tile_rows == 1) launch_simt<D, 1>(p, plan, stream);
     else if (plan.tile_rows == 2) launch_simt<D, 2>(p, plan, stream);
     else launch_simt<D, 4>(p, plan, stream);
     cudaError_t e = cudaGetLastError();

@@ -1,0 +1,649 @@
+// Attention over the history cache on the tensor cores: up to 128 query rows (tokens times
+// the heads that share a key/value head) of one sequence against 64 slots at a time. The
+// rule, the tiles and the splits are ba_cache_fwd.cu's.
+//
+// S = Q K^T and O += P V run as tcgen05 MMAs (M = 128 rows, bf16 operands, float32
+// accumulators in TMEM) whose A operands, Q and P, stay in TMEM: shared memory then carries
+// only the widened keys and values. Those are MX codes in the cache; the dequantising warps
+// load 16 codes a lane straight into registers, widen them to bf16 (exact: an E4M3 value has
+// four significant bits and the scale is a power of two) and store them in the MMA's
+// 128-byte-swizzled layout. A tensor product on the codes themselves would have to round Q
+// to E4M3, and the values' scales run along head_dim, not along the keys that P V sums over.
+// P is rounded to bf16 for its MMA, the running sum takes the unrounded probabilities.
+//
+// Roles of a block (288 threads, two blocks an SM, so that one block's softmax and set-up
+// overlap the other's MMAs):
+//   warps 0-3  softmax: thread t owns row t (TMEM lane t)
+//   warps 4-7  dequantisation, one 64-slot tile ahead of the MMAs in registers and up to
+//              kStages tiles in shared memory
+//   warp 8     MMA issue
+// TMEM columns: O at 0, S at 128 (P over its first 32), Q at 192.
+//
+// With selected pages the block first lists the units (pages, or halves of 128-slot pages)
+// that any of its rows sees, so that small pages far apart share a tile.
+#include "ba_cache_fwd.cuh"
+#include "ba_kernels.cuh"
+#include "ba_ptx.cuh"
+
+#include <type_traits>
+
+namespace ba {
+
+namespace {
+
+constexpr int kKeys = 64; // slots of a tile
+constexpr int kThreads = 288;
+
+template <int D>
+struct MmaLayout {
+    static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr int kChunkBytes = kKeys * 128;      // 64 slots x 64 columns, bf16
+    static constexpr int kTileBytes = kKeys * D * 2;
+    // K of stage s at 2 s tiles, V after it. 96 KB whatever D: two blocks an SM, never three,
+    // whose TMEM (256 columns each) would not fit
+    static constexpr int kBytes = 96 * 1024;
+    static_assert(2 * kStages * kTileBytes <= kBytes, "stages fit");
+    static constexpr int kAlloc = kBytes + 1024;
+    static constexpr uint32_t kTmemCols = 256, kColO = 0, kColS = 128, kColQ = 192;
+};
+
+struct MmaShared {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full, p_full, o_final;
+    uint32_t tmem;
+    int abort;
+    int32_t min_ws, max_pos; // over the tile's rows
+    int32_t nlist;
+    int32_t bad_pages;       // some page of the split has no number
+    int32_t odd_values;      // some value is NaN or infinite
+    uint32_t wanted[kMmaList / 32 + 1];
+    int32_t list[kMmaList];  // first slots of the listed units
+};
+
+// What a block's roles know of its slots.
+struct Slots {
+    int32_t from;    // first slot (no list)
+    int32_t unit;    // slots of a unit (no list: the whole tile)
+    int32_t end;     // slots at and past it do not exist
+    int32_t ntiles;
+    bool listed;
+};
+
+// First slot of unit k of tile i; past the list: INT32_MAX - 63.
+__device__ __forceinline__ int32_t unit_slot(const Slots &s, const MmaShared &sb, int32_t i, int32_t k)
+{
+    if (!s.listed) return s.from + i * kKeys + k * s.unit;
+    const int32_t x = i * (kKeys / s.unit) + k;
+    return x < sb.nlist ? sb.list[x] : INT32_MAX - 63;
+}
+
+// Bits lo .. hi (clamped to 0 .. n - 1) of a 64-bit word.
+__device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi, int32_t n)
+{
+    if (lo < 0) lo = 0;
+    if (hi > n - 1) hi = n - 1;
+    return lo <= hi ? (~uint64_t(0) >> (63 - hi)) & (~uint64_t(0) << lo) : 0;
+}
+
+// Which of the n slots from `us` on row r sees.
+__device__ __forceinline__ uint64_t visible_bits(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h,
+                                                 int32_t us, int32_t n, int32_t end, bool check_pages)
+{
+    if (us >= end) return 0;
+    int32_t ws = r.ws;
+    if (p.page_mask && us < t.len && us < ws) {
+        const int32_t page = us >> p.c.page_shift;
+        if ((__ldg(p.page_mask + ((int64_t(t.q0) + r.tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
+             (page & 31)) & 1u)
+            ws = 0;
+    }
+    uint64_t bits = bit_range(int64_t(ws) - us, int64_t(min(r.pos, t.len - 1)) - us, n);
+    if (us + n > t.len) {
+        if (!p.tree && !p.q.positions) {
+            bits |= bit_range(int64_t(max(r.ws, t.len)) - us, int64_t(min(r.pos, end - 1)) - us, n);
+        } else {
+            const int32_t stop = min(us + n, end);
+            for (int32_t s = max(us, t.len); s < stop; ++s)
+                if (sees(p, t, r, h, s)) bits |= uint64_t(1) << (s - us);
+        }
+    }
+    if (check_pages && bits) {
+        for (int32_t x = 0; x < n; x += 16)
+            if (cache_page(p.c, t.b, (us + x) >> p.c.page_shift) < 0) bits &= ~(uint64_t(0xffff) << x);
+    }
+    return bits;
+}
+
+// Sixteen E4M3 codes with the scale code of their block as bf16, exactly (the products
+// below bf16's normal range round to its subnormals). A code's sign, exponent and mantissa
+// moved to a bf16's places (sign to bit 15, the other seven bits to bits 10 .. 4) are the
+// value times 2^-120, subnormal codes included; one multiplication by 2^(e + 120) makes up
+// for that and applies the scale. Past 2^127 the factor is split in two. Returns whether a
+// code is NaN (which this arithmetic does not know).
+__device__ __forceinline__ bool widen16(const uint4 &codes, uint32_t scale_code, uint32_t (&out)[8])
+{
+    const uint32_t ws[4] = {codes.x, codes.y, codes.z, codes.w};
+    const uint32_t field = scale_code + 120;
+    const uint32_t f1 = (field < 254 ? field : 254u) * 0x00800080u;
+    __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162 *>(&f1);
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mag = ws[i] & 0x7f7f7f7fu, sign = ws[i] & 0x80808080u;
+        nan |= mag + 0x01010101u; // a NaN's byte becomes 0x80
+#pragma unroll
+        for (int hi = 0; hi < 2; ++hi) {
+            const uint32_t m = __byte_perm(mag, 0, hi ? 0x4342 : 0x4140), s = __byte_perm(sign, 0, hi ? 0x3424 : 0x1404);
+            const uint32_t x = (m << 4) + s;
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), s1);
+            out[2 * i + hi] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    }
+    if (field > 254) {
+        const uint32_t f2 = (field - 254 + 127) * 0x00800080u;
+        const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162 *>(&f2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&out[i]), s2);
+            out[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    }
+    return nan & 0x80808080u;
+}
+
+// Four codes with their widened form (two words), mended for what is rare (out of line, so
+// that the registers of the common path stay registers): NaNs are put in; with clear, NaNs
+// and infinities become 0 and *odd says that there were any.
+__device__ __noinline__ uint2 mend4(uint32_t codes, uint2 out, bool clear, int32_t *odd)
+{
+    uint32_t o[2] = {out.x, out.y};
+    for (int i = 0; i < 4; ++i) {
+        const int sh = 16 * (i % 2);
+        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) o[i / 2] |= 0x7fffu << sh;
+        if (clear && ((o[i / 2] >> sh) & 0x7f80u) == 0x7f80u) {
+            o[i / 2] &= ~(0xffffu << sh);
+            *odd = 1;
+        }
+    }
+    return make_uint2(o[0], o[1]);
+}
+
+// Columns of this row's output that a NaN, +infinity or -infinity among the values it sees
+// must reach. P V runs on values with those cleared, because a row that does not see them
+// would multiply them by zero; the rows that do are mended here, from the codes. Called by
+// whole warps, lane = row; one 4-byte word of codes a lane.
+template <int D>
+struct OddValues {
+    uint32_t nan[D / 32], pos[D / 32], neg[D / 32];
+};
+
+template <int D>
+__device__ __noinline__ void find_odd_values(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h,
+                                             const Slots &sl, const MmaShared &sb, OddValues<D> &odd)
+{
+    const int lane = threadIdx.x & 31;
+    for (int w = 0; w < D / 32; ++w) odd.nan[w] = odd.pos[w] = odd.neg[w] = 0;
+    for (int32_t i = 0; i < sl.ntiles; ++i)
+        for (int32_t c = 0; c < kKeys; ++c) {
+            const int32_t slot = unit_slot(sl, sb, i, c / sl.unit) + c % sl.unit;
+            if (slot >= sl.end) continue;
+            const int32_t id = cache_page(p.c, t.b, slot >> p.c.page_shift);
+            if (id < 0) continue;
+            const int64_t row = cache_row(p.c, id, h, slot & ((1 << p.c.page_shift) - 1));
+            uint32_t n = 0, a = 0, b = 0;
+            if (lane < D / 4) {
+                const uint32_t codes = __ldg(reinterpret_cast<const uint32_t *>(p.c.v + row * D) + lane);
+                const float s = mx_scale(__ldg(p.c.v_scales + row * (D / 32) + lane / 8));
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t code = (codes >> (8 * x)) & 0xffu;
+                    const float f = __bfloat162float(__float2bfloat16(e4m3x2_to_f32(code).x * s));
+                    n |= uint32_t(f != f) << x;
+                    a |= uint32_t(f == INFINITY) << x;
+                    b |= uint32_t(f == -INFINITY) << x;
+                }
+            }
+            if (!__any_sync(0xffffffffu, n | a | b)) continue;
+            const bool mine = sees(p, t, r, h, slot);
+            for (int w = 0; w < D / 32; ++w) {
+                const int sh = 4 * (lane % 8);
+                const bool here = lane / 8 == w;
+                const uint32_t nw = __reduce_or_sync(0xffffffffu, here ? n << sh : 0u);
+                const uint32_t aw = __reduce_or_sync(0xffffffffu, here ? a << sh : 0u);
+                const uint32_t bw = __reduce_or_sync(0xffffffffu, here ? b << sh : 0u);
+                if (mine) {
+                    odd.nan[w] |= nw;
+                    odd.pos[w] |= aw;
+                    odd.neg[w] |= bw;
+                }
+            }
+        }
+}
+
+} // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheFwd p)
+{
+    using Lay = MmaLayout<D>;
+    constexpr int S = Lay::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ MmaShared sb;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t smem_base = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t h = blockIdx.y, split = blockIdx.z;
+    FwdTile t;
+    if (!find_tile(p, kMmaRows, t)) return;
+    const int active = (t.rows + 31) / 32; // softmax warps with rows
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&sb.k_full[i], 4);
+            mbar_init(&sb.k_empty[i], 1);
+            mbar_init(&sb.v_full[i], 4);
+            mbar_init(&sb.v_empty[i], 1);
+        }
+        mbar_init(&sb.s_full, 1);
+        mbar_init(&sb.p_full, active);
+        mbar_init(&sb.o_final, 1);
+        sb.abort = 0;
+        sb.min_ws = INT32_MAX;
+        sb.max_pos = -1;
+        sb.nlist = 0;
+        sb.bad_pages = 0;
+        sb.odd_values = 0;
+        fence_mbar_init();
+    }
+    if (p.page_mask)
+        for (int i = tid; i < kMmaList / 32 + 1; i += kThreads) sb.wanted[i] = 0;
+    if (warp == 8) {
+        tmem_alloc(&sb.tmem, Lay::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sb.tmem;
+    volatile int *abort = &sb.abort;
+
+    const int32_t row = t.row0 + min(tid, t.rows - 1);
+    const RowView rv = row_view(p, t, row); // (warps past the rows: the last row's)
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    if (warp < active) {
+        const int32_t mw = __reduce_min_sync(0xffffffffu, rv.ws), mp = __reduce_max_sync(0xffffffffu, rv.pos);
+        if (lane == 0) {
+            atomicMin(&sb.min_ws, mw);
+            atomicMax(&sb.max_pos, mp);
+        }
+        // this row of Q into TMEM
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q.q + out_row(p, t, h, row) * D);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            uint32_t w[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint4 x = __ldg(src + 8 * c + u);
+                w[4 * u] = x.x, w[4 * u + 1] = x.y, w[4 * u + 2] = x.z, w[4 * u + 3] = x.w;
+            }
+            tmem_st32(tmem + lane_base + Lay::kColQ + 32 * c, w);
+        }
+        tmem_wait_st();
+    }
+    __syncthreads();
+
+    // this split's slots
+    Slots sl;
+    sl.listed = p.page_mask != nullptr;
+    const int32_t size = 1 << p.c.page_shift;
+    sl.unit = sl.listed ? min(size, kKeys) : kKeys;
+    sl.end = t.end;
+    if (!p.tree && !p.q.positions)
+        sl.end = int32_t(min(int64_t(t.end), int64_t(t.len) + (t.row0 + t.rows - 1) / p.q.group + 1));
+    const int32_t min_ws = sb.min_ws;
+    const int64_t from = (sl.listed ? 0 : min_ws / kKeys * kKeys) + int64_t(split) * p.chunk;
+    int64_t to = split + 1 == p.nsplit ? sl.end : from + p.chunk;
+    if (to > sl.end) to = sl.end;
+    sl.from = int32_t(min(from, int64_t(sl.end)));
+    sl.ntiles = from < to ? int32_t((to - from + kKeys - 1) / kKeys) : 0;
+    if (sl.listed) {
+        // bits of the pages from `from` on that a row selects, then the list of units
+        const int32_t page0 = sl.from >> p.c.page_shift;
+        const int32_t npages = from < to ? int32_t((to - 1) >> p.c.page_shift) - page0 + 1 : 0;
+        const int32_t tok0 = t.row0 / p.q.group, ntok = (t.row0 + t.rows - 1) / p.q.group - tok0 + 1;
+        const int32_t w0 = page0 >> 5, nw = npages > 0 ? ((page0 + npages - 1) >> 5) - w0 + 1 : 0;
+        for (int32_t x = tid; x < nw * ntok; x += kThreads) {
+            const int32_t w = x % nw, tok = tok0 + x / nw;
+            const uint32_t bits = __ldg(p.page_mask + ((int64_t(t.q0) + tok) * p.c.kv_heads + h) * p.mask_words + w0 + w);
+            if (bits) atomicOr(&sb.wanted[w], bits);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int32_t nunits = from < to ? int32_t((to - from + sl.unit - 1) / sl.unit) : 0;
+            int32_t count = 0;
+            for (int32_t u0 = 0; u0 < nunits; u0 += 32) {
+                const int32_t us = sl.from + (u0 + lane) * sl.unit;
+                bool want = false;
+                if (u0 + lane < nunits) {
+                    const int32_t page = us >> p.c.page_shift;
+                    const bool bit = (sb.wanted[(page >> 5) - w0] >> (page & 31)) & 1u;
+                    want = (us < t.len && us <= sb.max_pos && (bit || us + sl.unit > min_ws)) || us + sl.unit > t.len;
+                }
+                const uint32_t b = __ballot_sync(0xffffffffu, want);
+                if (want) sb.list[count + __popc(b & ((1u << lane) - 1))] = us;
+                count += __popc(b);
+            }
+            if (lane == 0) sb.nlist = count;
+        }
+        __syncthreads();
+        const int32_t per = kKeys / sl.unit;
+        sl.ntiles = (sb.nlist + per - 1) / per;
+    }
+    // pages without a number among them: their slots are unseen
+    {
+        const int32_t step = min(size, kKeys), per = kKeys / step;
+        for (int32_t x = tid; x < sl.ntiles * per; x += kThreads) {
+            const int32_t us = sl.listed ? unit_slot(sl, sb, x / per, x % per) : sl.from + x * step;
+            if (us < sl.end && cache_page(p.c, t.b, us >> p.c.page_shift) < 0) {
+                sb.bad_pages = 1;
+                cache_range_error(p.c);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+
+    if (warp < active) {
+        // ------------------------------------------------------ softmax ---
+        const bool valid = tid < t.rows;
+        const uint32_t s_addr = tmem + lane_base + Lay::kColS, o_addr = tmem + lane_base + Lay::kColO;
+        const bool check_pages = sb.bad_pages != 0;
+        float m_ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int32_t i = 0; i < sl.ntiles; ++i) {
+            uint64_t bits = 0;
+            if (!sl.listed) {
+                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end, check_pages);
+            } else {
+                for (int32_t k = 0; k < kKeys / sl.unit; ++k)
+                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), sl.unit, sl.end, check_pages)
+                            << (k * sl.unit);
+            }
+            const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
+            const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
+            if (!mbar_wait(&sb.s_full, i & 1, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t sr[2][32];
+            tmem_ld32(s_addr, sr[0]);
+            tmem_ld32(s_addr + 32, sr[1]);
+            tmem_wait_ld();
+            reg_fence(sr[0]);
+            reg_fence(sr[1]);
+            float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 2) {
+                float a = __uint_as_float(sr[c / 32][c % 32]), b = __uint_as_float(sr[c / 32][c % 32 + 1]);
+                if (!full) {
+                    a = (vis[c / 32] & (1u << (c % 32))) ? a : -INFINITY;
+                    b = (vis[c / 32] & (1u << (c % 32 + 1))) ? b : -INFINITY;
+                    sr[c / 32][c % 32] = __float_as_uint(a);
+                    sr[c / 32][c % 32 + 1] = __float_as_uint(b);
+                }
+                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], a, b);
+            }
+            const float m_new = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
+            // O and l move to the new maximum only when it grew by more than 2^8
+            float alpha = 1.f;
+            const bool grow = m_new > m_ref + 8.0f;
+            if (grow) {
+                alpha = ex2_approx(m_ref - m_new);
+                m_ref = m_new;
+            }
+            const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
+            float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            uint32_t pk[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float2 x = ffma2(make_float2(__uint_as_float(sr[c / 16][2 * (c % 16)]),
+                                                   __uint_as_float(sr[c / 16][2 * (c % 16) + 1])),
+                                       sc2, nm2);
+                const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                acc[c % 2] = fadd2(acc[c % 2], make_float2(p0, p1));
+                pk[c] = pack_bf16x2(p0, p1);
+            }
+            tmem_st32(s_addr, pk);
+            const float2 sum = fadd2(acc[0], acc[1]);
+            l = fmaf(l, alpha, sum.x + sum.y);
+            // O holds the earlier tiles' P V (complete: this S was issued after it)
+            if (i > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_addr + c * 32, o);
+                    tmem_wait_ld();
+                    reg_fence(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    tmem_st32(o_addr + c * 32, o);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.p_full);
+        }
+        // the last P V, and (for odd_values) what the dequantising warps wrote before it
+        if (ok && sl.ntiles > 0)
+            ok = mbar_wait(&sb.o_final, 0, abort) &&
+                 mbar_wait(&sb.v_full[(sl.ntiles - 1) % S], ((sl.ntiles - 1) / S) & 1, abort);
+        if (ok) {
+            tc_fence_after();
+            OddValues<D> odd;
+            const bool any_odd = sl.ntiles > 0 && *reinterpret_cast<volatile int32_t *>(&sb.odd_values);
+            if (any_odd) find_odd_values<D>(p, t, rv, h, sl, sb, odd);
+            const int64_t oh = out_row(p, t, h, row);
+            const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
+            const bool whole = p.nsplit == 1;
+            const int64_t at = whole ? oh : int64_t(split) * p.q.rows * heads + oh;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // a part without any visible slot is left out by its statistics
+            const bool store = valid && (whole || l != 0.f);
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (sl.ntiles > 0) {
+                    tmem_ld32(o_addr + c * 32, o);
+                    tmem_wait_ld();
+                    reg_fence(o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0;
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                if (any_odd) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const uint32_t b = 1u << k;
+                        const bool a = odd.pos[c] & b, n = odd.neg[c] & b;
+                        if (a) o[k] = 0x7f800000u;
+                        if (n) o[k] = 0xff800000u;
+                        if ((odd.nan[c] & b) || (a && n)) o[k] = 0x7fffffffu;
+                    }
+                }
+                if (store && whole) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + 32 * c);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        dst[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+                } else if (store) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * c);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                }
+            }
+            if (valid) {
+                if (whole) {
+                    const int64_t token = int64_t(t.q0) + row / p.q.group;
+                    p.lse[(int64_t(h) * p.q.group + row % p.q.group) * p.q.rows + token] =
+                        (m_ref + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    p.part_ml[at] = make_float2(m_ref, l);
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ----------------------------------------------- dequantisation ---
+        constexpr int kLanes = D / 16, kRows = 128 / kLanes, kU = kKeys / kRows;
+        const int x = tid - 128, col = x % kLanes, r0 = x / kLanes;
+        const int32_t in_page = size - 1;
+        // the two 16-byte units of this lane's 16 columns in a 128-byte row of their 64-column
+        // chunk; lanes of the upper chunk store them in the other order, so that eight
+        // consecutive lanes meet eight different units (no bank conflict)
+        const int flip = (col / 4) & 1, unit0 = (col % 4) * 2;
+        uint8_t *const chunk = smem + (col / 4) * Lay::kChunkBytes;
+        auto slot_of = [&](int32_t i, int u) {
+            const int r = r0 + kRows * u;
+            return unit_slot(sl, sb, i, r / sl.unit) + r % sl.unit;
+        };
+        auto page_of = [&](int32_t i, int u) -> int32_t {
+            const int32_t slot = slot_of(i, u);
+            return slot < sl.end ? cache_page(p.c, t.b, slot >> p.c.page_shift) : -1;
+        };
+        // pool row of (tile i, load u), -1: nothing there
+        auto row_of = [&](int32_t i, int u, int32_t id) -> int64_t {
+            return id < 0 ? -1 : cache_row(p.c, id, h, slot_of(i, u) & in_page);
+        };
+        auto load = [&](const uint8_t *codes, const uint8_t *scales, const int64_t (&rows)[kU], uint4 (&w)[kU],
+                        uint32_t (&sc)[kU]) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                w[u] = make_uint4(0u, 0u, 0u, 0u);
+                sc[u] = 127;
+                if (rows[u] >= 0) {
+                    w[u] = __ldg(reinterpret_cast<const uint4 *>(codes + rows[u] * D) + col);
+                    sc[u] = __ldg(scales + rows[u] * (D / 32) + col / 2);
+                }
+            }
+        };
+        auto store = [&](uint32_t offset, const uint4 (&w)[kU], const uint32_t (&sc)[kU], bool values) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                uint32_t o[8];
+                const bool nan = widen16(w[u], sc[u], o);
+                // (448 * 2^119 is finite; only larger scales' products can overflow)
+                if (nan || (values && sc[u] > 246)) {
+                    const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const uint2 y = mend4(ws[x], make_uint2(o[2 * x], o[2 * x + 1]), values, &sb.odd_values);
+                        o[2 * x] = y.x;
+                        o[2 * x + 1] = y.y;
+                    }
+                }
+                const int r = r0 + kRows * u;
+                uint8_t *dst = chunk + offset + r * 128;
+                const int ua = unit0 + flip, ub = unit0 + 1 - flip;
+                *reinterpret_cast<uint4 *>(dst + ((ua ^ (r & 7)) << 4)) =
+                    flip ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(dst + ((ub ^ (r & 7)) << 4)) =
+                    flip ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        int64_t rows[kU];
+        int32_t ids[kU];
+        uint4 kw[kU], vw[kU];
+        uint32_t ks[kU], vs[kU];
+        if (sl.ntiles > 0) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) rows[u] = row_of(0, u, page_of(0, u));
+            load(p.c.k, p.c.k_scales, rows, kw, ks);
+            load(p.c.v, p.c.v_scales, rows, vw, vs);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) ids[u] = sl.ntiles > 1 ? page_of(1, u) : -1;
+        for (int32_t i = 0; i < sl.ntiles; ++i) {
+            const int st = i % S;
+            const uint32_t parity = ((i / S) & 1) ^ 1;
+            const bool more = i + 1 < sl.ntiles;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                rows[u] = more ? row_of(i + 1, u, ids[u]) : -1;
+                ids[u] = i + 2 < sl.ntiles ? page_of(i + 2, u) : -1;
+            }
+            if (!mbar_wait(&sb.k_empty[st], parity, abort)) break;
+            store(2 * st * Lay::kTileBytes, kw, ks, false);
+            if (lane == 0) mbar_arrive(&sb.k_full[st]);
+            if (more) load(p.c.k, p.c.k_scales, rows, kw, ks);
+            if (!mbar_wait(&sb.v_empty[st], parity, abort)) break;
+            store((2 * st + 1) * Lay::kTileBytes, vw, vs, true);
+            if (lane == 0) mbar_arrive(&sb.v_full[st]);
+            if (more) load(p.c.v, p.c.v_scales, rows, vw, vs);
+        }
+    } else if (warp == 8) {
+        // ---------------------------------------------------- MMA issue ---
+        constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
+        constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+        for (int32_t i = 0; i < sl.ntiles; ++i) {
+            const int st = i % S;
+            const uint32_t parity = (i / S) & 1;
+            const uint32_t k_addr = smem_base + 2 * st * Lay::kTileBytes, v_addr = k_addr + Lay::kTileBytes;
+            if (!mbar_wait(&sb.k_full[st], parity, abort)) break;
+            tc_fence_after();
+            // S over the previous tile's P, whose P V was issued before it
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                mma_ts(tmem + Lay::kColS, tmem + Lay::kColQ + kk * 8,
+                       sdesc_sw128(k_addr + (kk / 4) * Lay::kChunkBytes + (kk % 4) * 32, 16, 1024), idesc_s,
+                       kk > 0 ? 1u : 0u);
+            tc_commit(&sb.s_full);
+            tc_commit(&sb.k_empty[st]);
+            __syncwarp();
+            if (!mbar_wait(&sb.p_full, i & 1, abort) || !mbar_wait(&sb.v_full[st], parity, abort)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts(tmem + Lay::kColO, tmem + Lay::kColS + kk * 8,
+                       sdesc_sw128(v_addr + kk * 2048, Lay::kChunkBytes, 1024), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(&sb.v_empty[st]);
+            if (i + 1 == sl.ntiles) tc_commit(&sb.o_final);
+            __syncwarp();
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, Lay::kTmemCols);
+    if (tid == 0 && sb.abort && p.c.status) atomicOr(p.c.status, kStatusTimeout);
+}
+
+template <int D>
+cudaError_t launch_cache_fwd_mma(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
+{
+    auto kern = cache_fwd_mma_kernel<D>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaLayout<D>::kAlloc);
+    if (e != cudaSuccess) return e;
+    const dim3 grid(unsigned(plan.tiles), unsigned(p.c.kv_heads), unsigned(p.nsplit));
+    kern<<<grid, kThreads, MmaLayout<D>::kAlloc, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template cudaError_t launch_cache_fwd_mma<64>(const CacheFwd &, const CacheFwdPlan &, cudaStream_t);
+template cudaError_t launch_cache_fwd_mma<128>(const CacheFwd &, const CacheFwdPlan &, cudaStream_t);
+
+} // namespace ba

@@ -379,7 +379,8 @@ ba_status ba_fwd_noalloc(const ba_problem *p, const void *q, const void *k, cons
  *    a page (skipped: nothing outside the pools is read or written),
  *    ba_device_status(status, stream) returns BA_ERR_INVALID_ARG.
  *  - page_size 16, 32, 64 or 128; head_dim 64 or 128 (else
- *    BA_ERR_UNSUPPORTED); kv_heads <= 65535; max_pages * page_size < 2^31.
+ *    BA_ERR_UNSUPPORTED); kv_heads <= 65535; max_pages * page_size <=
+ *    2^30.
  *
  * The calls take lengths and starts as DEVICE arrays, so they can be captured
  * into a graph and replayed while the histories grow.
@@ -398,7 +399,7 @@ typedef struct {
  * head_dim] tensors, float32 or bf16) is quantised into slot starts[b] + t.
  * Scale and elements as ba_mx_quantize's. A NaN does not count for its
  * block's scale and becomes E4M3's NaN; an infinity sets the scale to 2^120
- * and becomes the largest code (448). Rows whose slot is negative, past
+ * and becomes the largest code, 448 (which reads back as infinity). Rows whose slot is negative, past
  * max_pages or without a page are skipped, and the status word says so.
  *
  * ba_cache_read: the reverse: row t of sequence b of k and v receives slot
@@ -466,7 +467,7 @@ ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, cons
  *     (tree_mask NULL: j <= t).
  * tree_mask: DEVICE uint32 [total_tokens, tree_words], bit j % 32 of word
  * j / 32 for row j of the same sequence; rows past tree_words * 32 are not
- * seen. A row without tree_mask and positions is what ba_fwd computes for the
+ * seen. With page_mask, max_pages <= 16384 (else BA_ERR_UNSUPPORTED). A row without tree_mask and positions is what ba_fwd computes for the
  * event at that position, on the dequantised keys and values, and so is each
  * row of a tree for the history that ends in its path. out: DEVICE bf16 like
  * q; lse: DEVICE float32 [heads, total_tokens]. A row that sees nothing

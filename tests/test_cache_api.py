@@ -95,6 +95,7 @@ def test_select_limits():
     assert select(cache(), summaries=None) == ba.BA_ERR_INVALID_ARG
     assert select(cache(), mask=None) == ba.BA_ERR_INVALID_ARG
     assert select(cache(max_pages=16385)) == ba.BA_ERR_UNSUPPORTED
+    assert fwd(cache(max_pages=16385), mask=FAKE) == ba.BA_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("kw", [dict(tree=FAKE, tree_words=0), dict(tree_words=-1), dict(tree=FAKE + 2, tree_words=1),
