@@ -11,13 +11,16 @@
 // to E4M3, and the values' scales run along head_dim, not along the keys that P V sums over.
 // P is rounded to bf16 for its MMA, the running sum takes the unrounded probabilities.
 //
-// Roles of a block (288 threads, two blocks an SM, so that one block's softmax and set-up
+// Roles of a block (512 threads, two blocks an SM, so that one block's softmax and set-up
 // overlap the other's MMAs):
-//   warps 0-3  softmax: thread t owns row t (TMEM lane t)
-//   warps 4-7  dequantisation, one 64-slot tile ahead of the MMAs in registers and up to
-//              kStages tiles in shared memory
-//   warp 8     MMA issue
+//   warps 0-3   softmax: thread t owns row t (TMEM lane t)
+//   warps 4-11  dequantisation, one 64-slot tile ahead in registers and up to kStages tiles
+//               ahead of the MMAs in shared memory
+//   warp 12     MMA issue (13-15 only fill its warpgroup, whose registers go to the softmax)
 // TMEM columns: O at 0, S at 128 (P over its first 32), Q at 192.
+//
+// Columns are kept in the order that widening four codes at once gives, 0 2 1 3 within each
+// four: Q is put in the same order as it is loaded, O is put back as it is stored.
 //
 // With selected pages the block first lists the units (pages, or halves of 128-slot pages)
 // that any of its rows sees, so that small pages far apart share a tile.
@@ -32,7 +35,11 @@ namespace ba {
 namespace {
 
 constexpr int kKeys = 64; // slots of a tile
-constexpr int kThreads = 288;
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12;
+// registers a thread after the split (softmax, dequantisation, MMA warpgroup); two blocks of
+// 512 threads are launched with 64 each: 104 + 2 * 56 + 40 = 4 * 64
+constexpr uint32_t kRegsSoftmax = 104, kRegsDequant = 56, kRegsMma = 40;
 
 template <int D>
 struct MmaLayout {
@@ -49,7 +56,7 @@ struct MmaLayout {
 };
 
 struct MmaShared {
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t full[4], empty[4]; // stages of K and V
     uint64_t s_full, p_full, o_final;
     uint32_t tmem;
     int abort;
@@ -64,7 +71,7 @@ struct MmaShared {
 // What a block's roles know of its slots.
 struct Slots {
     int32_t from;    // first slot (no list)
-    int32_t unit;    // slots of a unit (no list: the whole tile)
+    int32_t shift;   // log2 of a unit's slots (no list: the whole tile is one)
     int32_t end;     // slots at and past it do not exist
     int32_t ntiles;
     bool listed;
@@ -73,8 +80,8 @@ struct Slots {
 // First slot of unit k of tile i; past the list: INT32_MAX - 63.
 __device__ __forceinline__ int32_t unit_slot(const Slots &s, const MmaShared &sb, int32_t i, int32_t k)
 {
-    if (!s.listed) return s.from + i * kKeys + k * s.unit;
-    const int32_t x = i * (kKeys / s.unit) + k;
+    if (!s.listed) return s.from + i * kKeys + (k << s.shift);
+    const int32_t x = i * (kKeys >> s.shift) + k;
     return x < sb.nlist ? sb.list[x] : INT32_MAX - 63;
 }
 
@@ -116,28 +123,28 @@ __device__ __forceinline__ uint64_t visible_bits(const CacheFwd &p, const FwdTil
 }
 
 // Sixteen E4M3 codes with the scale code of their block as bf16, exactly (the products
-// below bf16's normal range round to its subnormals). A code's sign, exponent and mantissa
-// moved to a bf16's places (sign to bit 15, the other seven bits to bits 10 .. 4) are the
-// value times 2^-120, subnormal codes included; one multiplication by 2^(e + 120) makes up
-// for that and applies the scale. Past 2^127 the factor is split in two. Returns whether a
-// code is NaN (which this arithmetic does not know).
+// below bf16's normal range round to its subnormals), columns in the order 0 2 1 3 within
+// each four. A code's sign, exponent and mantissa moved to a bf16's places (sign to bit 15,
+// the other seven bits to bits 10 .. 4) are the value times 2^-120, subnormal codes included;
+// one multiplication by 2^(e + 120) makes up for that and applies the scale. Past 2^127 the
+// factor is split in two. Returns whether a code is NaN (which this arithmetic does not know).
 __device__ __forceinline__ bool widen16(const uint4 &codes, uint32_t scale_code, uint32_t (&out)[8])
 {
     const uint32_t ws[4] = {codes.x, codes.y, codes.z, codes.w};
     const uint32_t field = scale_code + 120;
     const uint32_t f1 = (field < 254 ? field : 254u) * 0x00800080u;
-    __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162 *>(&f1);
+    const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162 *>(&f1);
     uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t mag = ws[i] & 0x7f7f7f7fu, sign = ws[i] & 0x80808080u;
-        nan |= mag + 0x01010101u; // a NaN's byte becomes 0x80
+        const uint32_t w = ws[i];
+        nan |= (w & 0x7f7f7f7fu) + 0x01010101u; // a NaN's byte becomes 0x80
+        const uint32_t x[2] = {((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u),
+                               ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u)};
 #pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-            const uint32_t m = __byte_perm(mag, 0, hi ? 0x4342 : 0x4140), s = __byte_perm(sign, 0, hi ? 0x3424 : 0x1404);
-            const uint32_t x = (m << 4) + s;
-            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), s1);
-            out[2 * i + hi] = *reinterpret_cast<const uint32_t *>(&v);
+        for (int j = 0; j < 2; ++j) {
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x[j]), s1);
+            out[2 * i + j] = *reinterpret_cast<const uint32_t *>(&v);
         }
     }
     if (field > 254) {
@@ -158,11 +165,11 @@ __device__ __forceinline__ bool widen16(const uint4 &codes, uint32_t scale_code,
 __device__ __noinline__ uint2 mend4(uint32_t codes, uint2 out, bool clear, int32_t *odd)
 {
     uint32_t o[2] = {out.x, out.y};
-    for (int i = 0; i < 4; ++i) {
-        const int sh = 16 * (i % 2);
-        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) o[i / 2] |= 0x7fffu << sh;
-        if (clear && ((o[i / 2] >> sh) & 0x7f80u) == 0x7f80u) {
-            o[i / 2] &= ~(0xffffu << sh);
+    for (int i = 0; i < 4; ++i) { // code i is in word i % 2, half i / 2
+        const int sh = 16 * (i / 2);
+        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) o[i % 2] |= 0x7fffu << sh;
+        if (clear && ((o[i % 2] >> sh) & 0x7f80u) == 0x7f80u) {
+            o[i % 2] &= ~(0xffffu << sh);
             *odd = 1;
         }
     }
@@ -186,7 +193,7 @@ __device__ __noinline__ void find_odd_values(const CacheFwd &p, const FwdTile &t
     for (int w = 0; w < D / 32; ++w) odd.nan[w] = odd.pos[w] = odd.neg[w] = 0;
     for (int32_t i = 0; i < sl.ntiles; ++i)
         for (int32_t c = 0; c < kKeys; ++c) {
-            const int32_t slot = unit_slot(sl, sb, i, c / sl.unit) + c % sl.unit;
+            const int32_t slot = unit_slot(sl, sb, i, c >> sl.shift) + (c & ((1 << sl.shift) - 1));
             if (slot >= sl.end) continue;
             const int32_t id = cache_page(p.c, t.b, slot >> p.c.page_shift);
             if (id < 0) continue;
@@ -223,7 +230,7 @@ __device__ __noinline__ void find_odd_values(const CacheFwd &p, const FwdTile &t
 } // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheFwd p)
+__global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid_constant__ CacheFwd p)
 {
     using Lay = MmaLayout<D>;
     constexpr int S = Lay::kStages;
@@ -239,10 +246,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&sb.k_full[i], 4);
-            mbar_init(&sb.k_empty[i], 1);
-            mbar_init(&sb.v_full[i], 4);
-            mbar_init(&sb.v_empty[i], 1);
+            mbar_init(&sb.full[i], 8);
+            mbar_init(&sb.empty[i], 1);
         }
         mbar_init(&sb.s_full, 1);
         mbar_init(&sb.p_full, active);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
     }
     if (p.page_mask)
         for (int i = tid; i < kMmaList / 32 + 1; i += kThreads) sb.wanted[i] = 0;
-    if (warp == 8) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&sb.tmem, Lay::kTmemCols);
         tmem_relinquish();
     }
@@ -284,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const uint4 x = __ldg(src + 8 * c + u);
-                w[4 * u] = x.x, w[4 * u + 1] = x.y, w[4 * u + 2] = x.z, w[4 * u + 3] = x.w;
+                w[4 * u] = __byte_perm(x.x, x.y, 0x5410), w[4 * u + 1] = __byte_perm(x.x, x.y, 0x7632);
+                w[4 * u + 2] = __byte_perm(x.z, x.w, 0x5410), w[4 * u + 3] = __byte_perm(x.z, x.w, 0x7632);
             }
             tmem_st32(tmem + lane_base + Lay::kColQ + 32 * c, w);
         }
@@ -296,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
     Slots sl;
     sl.listed = p.page_mask != nullptr;
     const int32_t size = 1 << p.c.page_shift;
-    sl.unit = sl.listed ? min(size, kKeys) : kKeys;
+    sl.shift = sl.listed ? min(p.c.page_shift, 6) : 6;
+    const int32_t unit = 1 << sl.shift;
     sl.end = t.end;
     if (!p.tree && !p.q.positions)
         sl.end = int32_t(min(int64_t(t.end), int64_t(t.len) + (t.row0 + t.rows - 1) / p.q.group + 1));
@@ -319,15 +326,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
         }
         __syncthreads();
         if (warp == 0) {
-            const int32_t nunits = from < to ? int32_t((to - from + sl.unit - 1) / sl.unit) : 0;
+            const int32_t nunits = from < to ? int32_t((to - from + unit - 1) >> sl.shift) : 0;
             int32_t count = 0;
             for (int32_t u0 = 0; u0 < nunits; u0 += 32) {
-                const int32_t us = sl.from + (u0 + lane) * sl.unit;
+                const int32_t us = sl.from + ((u0 + lane) << sl.shift);
                 bool want = false;
                 if (u0 + lane < nunits) {
                     const int32_t page = us >> p.c.page_shift;
                     const bool bit = (sb.wanted[(page >> 5) - w0] >> (page & 31)) & 1u;
-                    want = (us < t.len && us <= sb.max_pos && (bit || us + sl.unit > min_ws)) || us + sl.unit > t.len;
+                    want = (us < t.len && us <= sb.max_pos && (bit || us + unit > min_ws)) || us + unit > t.len;
                 }
                 const uint32_t b = __ballot_sync(0xffffffffu, want);
                 if (want) sb.list[count + __popc(b & ((1u << lane) - 1))] = us;
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
             if (lane == 0) sb.nlist = count;
         }
         __syncthreads();
-        const int32_t per = kKeys / sl.unit;
+        const int32_t per = kKeys >> sl.shift;
         sl.ntiles = (sb.nlist + per - 1) / per;
     }
     // pages without a number among them: their slots are unseen
@@ -354,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
     __syncthreads();
     tc_fence_after();
 
-    if (warp < active) {
+    if (warp < 4) {
+        warpgroup_regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------ softmax ---
+        if (warp < active) {
         const bool valid = tid < t.rows;
         const uint32_t s_addr = tmem + lane_base + Lay::kColS, o_addr = tmem + lane_base + Lay::kColO;
         const bool check_pages = sb.bad_pages != 0;
@@ -366,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
             if (!sl.listed) {
                 bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end, check_pages);
             } else {
-                for (int32_t k = 0; k < kKeys / sl.unit; ++k)
-                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), sl.unit, sl.end, check_pages)
-                            << (k * sl.unit);
+                for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
+                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end, check_pages)
+                            << (k << sl.shift);
             }
             const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
             const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
@@ -383,18 +392,16 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
             tmem_wait_ld();
             reg_fence(sr[0]);
             reg_fence(sr[1]);
+            if (!full) {
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c)
+                    sr[c / 32][c % 32] = (vis[c / 32] & (1u << (c % 32))) ? sr[c / 32][c % 32] : 0xff800000u;
+            }
             float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 2) {
-                float a = __uint_as_float(sr[c / 32][c % 32]), b = __uint_as_float(sr[c / 32][c % 32 + 1]);
-                if (!full) {
-                    a = (vis[c / 32] & (1u << (c % 32))) ? a : -INFINITY;
-                    b = (vis[c / 32] & (1u << (c % 32 + 1))) ? b : -INFINITY;
-                    sr[c / 32][c % 32] = __float_as_uint(a);
-                    sr[c / 32][c % 32 + 1] = __float_as_uint(b);
-                }
-                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], a, b);
-            }
+            for (int c = 0; c < kKeys; c += 2)
+                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], __uint_as_float(sr[c / 32][c % 32]),
+                                        __uint_as_float(sr[c / 32][c % 32 + 1]));
             const float m_new = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
             // O and l move to the new maximum only when it grew by more than 2^8
             float alpha = 1.f;
@@ -440,12 +447,19 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
         // the last P V, and (for odd_values) what the dequantising warps wrote before it
         if (ok && sl.ntiles > 0)
             ok = mbar_wait(&sb.o_final, 0, abort) &&
-                 mbar_wait(&sb.v_full[(sl.ntiles - 1) % S], ((sl.ntiles - 1) / S) & 1, abort);
+                 mbar_wait(&sb.full[(sl.ntiles - 1) % S], ((sl.ntiles - 1) / S) & 1, abort);
         if (ok) {
             tc_fence_after();
             OddValues<D> odd;
             const bool any_odd = sl.ntiles > 0 && *reinterpret_cast<volatile int32_t *>(&sb.odd_values);
-            if (any_odd) find_odd_values<D>(p, t, rv, h, sl, sb, odd);
+            if (any_odd) { // (copies: objects whose address is taken would live in memory throughout)
+                const FwdTile t2 = t;
+                const RowView r2 = rv;
+                const Slots s2 = sl;
+                OddValues<D> o2;
+                find_odd_values<D>(p, t2, r2, h, s2, sb, o2);
+                odd = o2;
+            }
             const int64_t oh = out_row(p, t, h, row);
             const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
             const bool whole = p.nsplit == 1;
@@ -467,6 +481,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
                     o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) { // 0 2 1 3 back to 0 1 2 3
+                    const uint32_t x = o[k + 1];
+                    o[k + 1] = o[k + 2];
+                    o[k + 2] = x;
+                }
                 if (any_odd) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
@@ -503,105 +523,99 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
                 }
             }
         }
-    } else if (warp >= 4 && warp < 8) {
+        }
+    } else if (warp < kMmaWarp) {
+        warpgroup_regs_dec<kRegsDequant>();
         // ----------------------------------------------- dequantisation ---
-        constexpr int kLanes = D / 16, kRows = 128 / kLanes, kU = kKeys / kRows;
+        constexpr int kLanes = D / 16, kRows = 256 / kLanes, kU = kKeys / kRows;
         const int x = tid - 128, col = x % kLanes, r0 = x / kLanes;
-        const int32_t in_page = size - 1;
         // the two 16-byte units of this lane's 16 columns in a 128-byte row of their 64-column
         // chunk; lanes of the upper chunk store them in the other order, so that eight
         // consecutive lanes meet eight different units (no bank conflict)
-        const int flip = (col / 4) & 1, unit0 = (col % 4) * 2;
-        uint8_t *const chunk = smem + (col / 4) * Lay::kChunkBytes;
+        const int flip = (col / 4) & 1, ua = (col % 4) * 2 + flip, ub = (col % 4) * 2 + 1 - flip;
+        uint8_t *const chunk = smem + (col / 4) * Lay::kChunkBytes + r0 * 128;
+        // bytes of a page, and this lane's first byte in it
+        const uint32_t page_bytes = uint32_t(p.c.kv_heads * D) << p.c.page_shift;
+        const uint32_t head_at = (uint32_t(h * D) << p.c.page_shift) + col * 16;
         auto slot_of = [&](int32_t i, int u) {
             const int r = r0 + kRows * u;
-            return unit_slot(sl, sb, i, r / sl.unit) + r % sl.unit;
+            return unit_slot(sl, sb, i, r >> sl.shift) + (r & (unit - 1));
         };
-        auto page_of = [&](int32_t i, int u) -> int32_t {
+        // the page table's entry for (tile i, load u), not checked yet; -1: no such slot
+        auto entry_of = [&](int32_t i, int u) -> int32_t {
+            if (i >= sl.ntiles) return -1;
             const int32_t slot = slot_of(i, u);
-            return slot < sl.end ? cache_page(p.c, t.b, slot >> p.c.page_shift) : -1;
+            return slot < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (slot >> p.c.page_shift))
+                                 : -1;
         };
-        // pool row of (tile i, load u), -1: nothing there
-        auto row_of = [&](int32_t i, int u, int32_t id) -> int64_t {
-            return id < 0 ? -1 : cache_row(p.c, id, h, slot_of(i, u) & in_page);
-        };
-        auto load = [&](const uint8_t *codes, const uint8_t *scales, const int64_t (&rows)[kU], uint4 (&w)[kU],
-                        uint32_t (&sc)[kU]) {
+        uint4 kw[kU], vw[kU];
+        uint32_t ks[kU], vs[kU];
+        int32_t ids[kU];
+        // codes and scale codes of tile i (page numbers in ids), zeros where there is no slot or page
+        auto load = [&](int32_t i) {
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                w[u] = make_uint4(0u, 0u, 0u, 0u);
-                sc[u] = 127;
-                if (rows[u] >= 0) {
-                    w[u] = __ldg(reinterpret_cast<const uint4 *>(codes + rows[u] * D) + col);
-                    sc[u] = __ldg(scales + rows[u] * (D / 32) + col / 2);
+                kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
+                ks[u] = vs[u] = 127;
+                if (uint32_t(ids[u]) < uint32_t(p.c.num_pages)) {
+                    const uint32_t in = head_at + uint32_t(slot_of(i, u) & (size - 1)) * D;
+                    const int64_t at = int64_t(ids[u]) * page_bytes + in;
+                    kw[u] = __ldg(reinterpret_cast<const uint4 *>(p.c.k + at));
+                    ks[u] = __ldg(p.c.k_scales + (at >> 5));
+                    vw[u] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + at));
+                    vs[u] = __ldg(p.c.v_scales + (at >> 5));
                 }
             }
         };
-        auto store = [&](uint32_t offset, const uint4 (&w)[kU], const uint32_t (&sc)[kU], bool values) {
+        auto store = [&](uint8_t *dst, const uint4 &w, uint32_t sc, bool values) {
+            uint32_t o[8];
+            const bool nan = widen16(w, sc, o);
+            // (448 * 2^119 is finite; only larger scales' products can overflow)
+            if (nan || (values && sc > 246)) {
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint2 z = mend4(ws[y], make_uint2(o[2 * y], o[2 * y + 1]), values, &sb.odd_values);
+                    o[2 * y] = z.x;
+                    o[2 * y + 1] = z.y;
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst + ((ua ^ (r0 & 7)) << 4)) =
+                flip ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + ((ub ^ (r0 & 7)) << 4)) =
+                flip ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        static_assert(kRows % 8 == 0, "a lane's rows swizzle alike");
+#pragma unroll
+        for (int u = 0; u < kU; ++u) ids[u] = entry_of(0, u);
+        load(0);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) ids[u] = entry_of(1, u);
+        for (int32_t i = 0; i < sl.ntiles; ++i) {
+            const int st = i % S;
+            if (!mbar_wait(&sb.empty[st], ((i / S) & 1) ^ 1, abort)) break;
+            uint8_t *dst = chunk + 2 * st * Lay::kTileBytes;
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                uint32_t o[8];
-                const bool nan = widen16(w[u], sc[u], o);
-                // (448 * 2^119 is finite; only larger scales' products can overflow)
-                if (nan || (values && sc[u] > 246)) {
-                    const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint2 y = mend4(ws[x], make_uint2(o[2 * x], o[2 * x + 1]), values, &sb.odd_values);
-                        o[2 * x] = y.x;
-                        o[2 * x + 1] = y.y;
-                    }
-                }
-                const int r = r0 + kRows * u;
-                uint8_t *dst = chunk + offset + r * 128;
-                const int ua = unit0 + flip, ub = unit0 + 1 - flip;
-                *reinterpret_cast<uint4 *>(dst + ((ua ^ (r & 7)) << 4)) =
-                    flip ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(dst + ((ub ^ (r & 7)) << 4)) =
-                    flip ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+                store(dst + u * kRows * 128, kw[u], ks[u], false);
+                store(dst + Lay::kTileBytes + u * kRows * 128, vw[u], vs[u], true);
             }
             fence_proxy_async_smem();
             __syncwarp();
-        };
-        int64_t rows[kU];
-        int32_t ids[kU];
-        uint4 kw[kU], vw[kU];
-        uint32_t ks[kU], vs[kU];
-        if (sl.ntiles > 0) {
+            if (lane == 0) mbar_arrive(&sb.full[st]);
+            load(i + 1);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) rows[u] = row_of(0, u, page_of(0, u));
-            load(p.c.k, p.c.k_scales, rows, kw, ks);
-            load(p.c.v, p.c.v_scales, rows, vw, vs);
+            for (int u = 0; u < kU; ++u) ids[u] = entry_of(i + 2, u);
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) ids[u] = sl.ntiles > 1 ? page_of(1, u) : -1;
-        for (int32_t i = 0; i < sl.ntiles; ++i) {
-            const int st = i % S;
-            const uint32_t parity = ((i / S) & 1) ^ 1;
-            const bool more = i + 1 < sl.ntiles;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                rows[u] = more ? row_of(i + 1, u, ids[u]) : -1;
-                ids[u] = i + 2 < sl.ntiles ? page_of(i + 2, u) : -1;
-            }
-            if (!mbar_wait(&sb.k_empty[st], parity, abort)) break;
-            store(2 * st * Lay::kTileBytes, kw, ks, false);
-            if (lane == 0) mbar_arrive(&sb.k_full[st]);
-            if (more) load(p.c.k, p.c.k_scales, rows, kw, ks);
-            if (!mbar_wait(&sb.v_empty[st], parity, abort)) break;
-            store((2 * st + 1) * Lay::kTileBytes, vw, vs, true);
-            if (lane == 0) mbar_arrive(&sb.v_full[st]);
-            if (more) load(p.c.v, p.c.v_scales, rows, vw, vs);
-        }
-    } else if (warp == 8) {
+    } else {
+        warpgroup_regs_dec<kRegsMma>();
         // ---------------------------------------------------- MMA issue ---
         constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
         constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-        for (int32_t i = 0; i < sl.ntiles; ++i) {
+        for (int32_t i = 0; warp == kMmaWarp && i < sl.ntiles; ++i) {
             const int st = i % S;
-            const uint32_t parity = (i / S) & 1;
             const uint32_t k_addr = smem_base + 2 * st * Lay::kTileBytes, v_addr = k_addr + Lay::kTileBytes;
-            if (!mbar_wait(&sb.k_full[st], parity, abort)) break;
+            if (!mbar_wait(&sb.full[st], (i / S) & 1, abort)) break;
             tc_fence_after();
             // S over the previous tile's P, whose P V was issued before it
 #pragma unroll
@@ -610,15 +624,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
                        sdesc_sw128(k_addr + (kk / 4) * Lay::kChunkBytes + (kk % 4) * 32, 16, 1024), idesc_s,
                        kk > 0 ? 1u : 0u);
             tc_commit(&sb.s_full);
-            tc_commit(&sb.k_empty[st]);
             __syncwarp();
-            if (!mbar_wait(&sb.p_full, i & 1, abort) || !mbar_wait(&sb.v_full[st], parity, abort)) break;
+            if (!mbar_wait(&sb.p_full, i & 1, abort)) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
                 mma_ts(tmem + Lay::kColO, tmem + Lay::kColS + kk * 8,
                        sdesc_sw128(v_addr + kk * 2048, Lay::kChunkBytes, 1024), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(&sb.v_empty[st]);
+            tc_commit(&sb.empty[st]);
             if (i + 1 == sl.ntiles) tc_commit(&sb.o_final);
             __syncwarp();
         }
@@ -627,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const CacheF
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, Lay::kTmemCols);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, Lay::kTmemCols);
     if (tid == 0 && sb.abort && p.c.status) atomicOr(p.c.status, kStatusTimeout);
 }
 
@@ -635,9 +648,14 @@ template <int D>
 cudaError_t launch_cache_fwd_mma(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
 {
     auto kern = cache_fwd_mma_kernel<D>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaLayout<D>::kAlloc);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MmaLayout<D>::kAlloc);
     if (e != cudaSuccess) return e;
+    // the register split only works if the block is launched with at least the budgets' sum
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kThreads < int(128 * (kRegsSoftmax + 2 * kRegsDequant + kRegsMma)))
+        return cudaErrorInvalidConfiguration;
     const dim3 grid(unsigned(plan.tiles), unsigned(p.c.kv_heads), unsigned(p.nsplit));
     kern<<<grid, kThreads, MmaLayout<D>::kAlloc, stream>>>(p);
     return cudaGetLastError();
