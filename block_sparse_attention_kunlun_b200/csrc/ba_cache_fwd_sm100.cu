@@ -4,19 +4,22 @@
 //
 // S = Q K^T and O += P V run as tcgen05 MMAs (M = 128 rows, bf16 operands, float32
 // accumulators in TMEM) whose A operands, Q and P, stay in TMEM: shared memory then carries
-// only the widened keys and values. Those are MX codes in the cache; the dequantising warps
-// load 16 codes a lane straight into registers, widen them to bf16 (exact: an E4M3 value has
-// four significant bits and the scale is a power of two) and store them in the MMA's
-// 128-byte-swizzled layout. A tensor product on the codes themselves would have to round Q
+// only keys and values. Those are MX codes in the cache. A head's slots of a page are
+// consecutive, so bulk copies bring codes and scales of 64 slots into shared memory with no
+// registers held meanwhile (loads into registers, one tile ahead, left the dequantising warps
+// waiting: 3200 cycles a tile); the dequantising warps widen them to bf16 (exact: an E4M3
+// value has four significant bits and the scale is a power of two) and store them in the
+// MMA's 128-byte-swizzled layout. A tensor product on the codes themselves would have to round Q
 // to E4M3, and the values' scales run along head_dim, not along the keys that P V sums over.
 // P is rounded to bf16 for its MMA, the running sum takes the unrounded probabilities.
 //
 // Roles of a block (512 threads, two blocks an SM, so that one block's softmax and set-up
 // overlap the other's MMAs):
 //   warps 0-3   softmax: thread t owns row t (TMEM lane t)
-//   warps 4-11  dequantisation, one 64-slot tile ahead in registers and up to kStages tiles
-//               ahead of the MMAs in shared memory
-//   warp 12     MMA issue (13-15 only fill its warpgroup, whose registers go to the softmax)
+//   warps 4-11  dequantisation of a 64-slot tile
+//   warp 12     MMA issue
+//   warp 13     bulk copies of the tiles' codes (14 and 15 only fill the warpgroup, whose
+//               registers go to the softmax)
 // TMEM columns: O at 0, S at 128 (P over its first 32), Q at 192.
 //
 // Columns are kept in the order that widening four codes at once gives, 0 2 1 3 within each
@@ -36,7 +39,7 @@ namespace {
 
 constexpr int kKeys = 64; // slots of a tile
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12;
+constexpr int kMmaWarp = 12, kCopyWarp = 13;
 // registers a thread after the split (softmax, dequantisation, MMA warpgroup); two blocks of
 // 512 threads are launched with 64 each: 104 + 2 * 56 + 40 = 4 * 64
 constexpr uint32_t kRegsSoftmax = 104, kRegsDequant = 56, kRegsMma = 40;
@@ -44,25 +47,29 @@ constexpr uint32_t kRegsSoftmax = 104, kRegsDequant = 56, kRegsMma = 40;
 template <int D>
 struct MmaLayout {
     static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-    static constexpr int kStages = D == 128 ? 3 : 4;
+    // stages of widened tiles (K, then V) and of codes (K, V, K scales, V scales): 97 KB for
+    // either D, so that two blocks fit an SM and never three, whose TMEM (256 columns each) would not
+    static constexpr int kStages = D == 128 ? 2 : 4, kRawStages = kStages;
     static constexpr int kChunkBytes = kKeys * 128;      // 64 slots x 64 columns, bf16
     static constexpr int kTileBytes = kKeys * D * 2;
-    // K of stage s at 2 s tiles, V after it. 96 KB whatever D: two blocks an SM, never three,
-    // whose TMEM (256 columns each) would not fit
-    static constexpr int kBytes = 96 * 1024;
-    static_assert(2 * kStages * kTileBytes <= kBytes, "stages fit");
+    static constexpr int kRaw0 = 2 * kStages * kTileBytes;
+    static constexpr int kRawV = kKeys * D, kRawKs = 2 * kRawV, kRawVs = kRawKs + kRawV / 32;
+    static constexpr int kRawBytes = 2 * kRawV + 2 * kRawV / 32;
+    static constexpr int kBytes = kRaw0 + kRawStages * kRawBytes;
     static constexpr int kAlloc = kBytes + 1024;
     static constexpr uint32_t kTmemCols = 256, kColO = 0, kColS = 128, kColQ = 192;
 };
 
 struct MmaShared {
-    uint64_t full[4], empty[4]; // stages of K and V
+    uint64_t full[4], empty[4];         // stages of widened K and V
+    uint64_t raw_full[4], raw_empty[4]; // stages of codes
+    // per tile (mod 16, more than can be under way): how many slots of each 16 there are, a byte each
+    uint32_t there[16];
     uint64_t s_full, p_full, o_final;
     uint32_t tmem;
     int abort;
     int32_t min_ws, max_pos; // over the tile's rows
     int32_t nlist;
-    int32_t bad_pages;       // some page of the split has no number
     int32_t odd_values;      // some value is NaN or infinite
     uint32_t wanted[kMmaList / 32 + 1];
     int32_t list[kMmaList];  // first slots of the listed units
@@ -95,7 +102,7 @@ __device__ __forceinline__ uint64_t bit_range(int64_t lo, int64_t hi, int32_t n)
 
 // Which of the n slots from `us` on row r sees.
 __device__ __forceinline__ uint64_t visible_bits(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h,
-                                                 int32_t us, int32_t n, int32_t end, bool check_pages)
+                                                 int32_t us, int32_t n, int32_t end)
 {
     if (us >= end) return 0;
     int32_t ws = r.ws;
@@ -106,18 +113,32 @@ __device__ __forceinline__ uint64_t visible_bits(const CacheFwd &p, const FwdTil
             ws = 0;
     }
     uint64_t bits = bit_range(int64_t(ws) - us, int64_t(min(r.pos, t.len - 1)) - us, n);
-    if (us + n > t.len) {
+    if (us + n > t.len) { // the unit holds drafted rows: slots first .. stop - 1
+        const int32_t first = max(us, t.len), stop = min(us + n, end);
         if (!p.tree && !p.q.positions) {
             bits |= bit_range(int64_t(max(r.ws, t.len)) - us, int64_t(min(r.pos, end - 1)) - us, n);
         } else {
-            const int32_t stop = min(us + n, end);
-            for (int32_t s = max(us, t.len); s < stop; ++s)
-                if (sees(p, t, r, h, s)) bits |= uint64_t(1) << (s - us);
+            // rows by the tree (or before this one), then their positions one by one
+            uint64_t rows = bit_range(first - us, stop - 1 - us, n);
+            if (!p.tree) {
+                rows &= bit_range(0, int64_t(t.len) + r.tok - us, n);
+            } else {
+                uint64_t sees = 0;
+                const uint32_t *words = p.tree + (int64_t(t.q0) + r.tok) * p.tree_words;
+                for (int32_t w = (first - t.len) >> 5; w <= (stop - 1 - t.len) >> 5 && w < p.tree_words; ++w) {
+                    const int32_t at = t.len + 32 * w - us; // the unit's bit of the word's first row
+                    const uint64_t word = __ldg(words + w);
+                    sees |= at >= 0 ? word << at : word >> -at;
+                }
+                rows &= sees;
+            }
+            for (uint64_t left = rows; left; left &= left - 1) {
+                const int32_t x = __ffsll(int64_t(left)) - 1;
+                const int32_t pj = query_position(p.q, t.q0, t.len, us + x - t.len);
+                if (pj > r.pos || pj < r.ws) rows &= ~(uint64_t(1) << x);
+            }
+            bits |= rows;
         }
-    }
-    if (check_pages && bits) {
-        for (int32_t x = 0; x < n; x += 16)
-            if (cache_page(p.c, t.b, (us + x) >> p.c.page_shift) < 0) bits &= ~(uint64_t(0xffff) << x);
     }
     return bits;
 }
@@ -248,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         for (int i = 0; i < S; ++i) {
             mbar_init(&sb.full[i], 8);
             mbar_init(&sb.empty[i], 1);
+            mbar_init(&sb.raw_full[i], 1);
+            mbar_init(&sb.raw_empty[i], 8);
         }
         mbar_init(&sb.s_full, 1);
         mbar_init(&sb.p_full, active);
@@ -256,7 +279,6 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         sb.min_ws = INT32_MAX;
         sb.max_pos = -1;
         sb.nlist = 0;
-        sb.bad_pages = 0;
         sb.odd_values = 0;
         fence_mbar_init();
     }
@@ -346,17 +368,6 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         const int32_t per = kKeys >> sl.shift;
         sl.ntiles = (sb.nlist + per - 1) / per;
     }
-    // pages without a number among them: their slots are unseen
-    {
-        const int32_t step = min(size, kKeys), per = kKeys / step;
-        for (int32_t x = tid; x < sl.ntiles * per; x += kThreads) {
-            const int32_t us = sl.listed ? unit_slot(sl, sb, x / per, x % per) : sl.from + x * step;
-            if (us < sl.end && cache_page(p.c, t.b, us >> p.c.page_shift) < 0) {
-                sb.bad_pages = 1;
-                cache_range_error(p.c);
-            }
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -367,18 +378,26 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         if (warp < active) {
         const bool valid = tid < t.rows;
         const uint32_t s_addr = tmem + lane_base + Lay::kColS, o_addr = tmem + lane_base + Lay::kColO;
-        const bool check_pages = sb.bad_pages != 0;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         for (int32_t i = 0; i < sl.ntiles; ++i) {
             uint64_t bits = 0;
             if (!sl.listed) {
-                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end, check_pages);
+                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end);
             } else {
                 for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
-                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end, check_pages)
+                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end)
                             << (k << sl.shift);
             }
+            // slots whose page has no number are unseen
+            if (!mbar_wait(&sb.full[i % S], (i / S) & 1, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t there = sb.there[i % 16];
+            if (there != 0x10101010u)
+                for (int g = 0; g < 4; ++g)
+                    if (((there >> (8 * g)) & 0xffu) == 0) bits &= ~(uint64_t(0xffff) << (16 * g));
             const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
             const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
             if (!mbar_wait(&sb.s_full, i & 1, abort)) {
@@ -444,10 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.p_full);
         }
-        // the last P V, and (for odd_values) what the dequantising warps wrote before it
-        if (ok && sl.ntiles > 0)
-            ok = mbar_wait(&sb.o_final, 0, abort) &&
-                 mbar_wait(&sb.full[(sl.ntiles - 1) % S], ((sl.ntiles - 1) / S) & 1, abort);
+        if (ok && sl.ntiles > 0) ok = mbar_wait(&sb.o_final, 0, abort);
         if (ok) {
             tc_fence_after();
             OddValues<D> odd;
@@ -534,39 +550,6 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         // consecutive lanes meet eight different units (no bank conflict)
         const int flip = (col / 4) & 1, ua = (col % 4) * 2 + flip, ub = (col % 4) * 2 + 1 - flip;
         uint8_t *const chunk = smem + (col / 4) * Lay::kChunkBytes + r0 * 128;
-        // bytes of a page, and this lane's first byte in it
-        const uint32_t page_bytes = uint32_t(p.c.kv_heads * D) << p.c.page_shift;
-        const uint32_t head_at = (uint32_t(h * D) << p.c.page_shift) + col * 16;
-        auto slot_of = [&](int32_t i, int u) {
-            const int r = r0 + kRows * u;
-            return unit_slot(sl, sb, i, r >> sl.shift) + (r & (unit - 1));
-        };
-        // the page table's entry for (tile i, load u), not checked yet; -1: no such slot
-        auto entry_of = [&](int32_t i, int u) -> int32_t {
-            if (i >= sl.ntiles) return -1;
-            const int32_t slot = slot_of(i, u);
-            return slot < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (slot >> p.c.page_shift))
-                                 : -1;
-        };
-        uint4 kw[kU], vw[kU];
-        uint32_t ks[kU], vs[kU];
-        int32_t ids[kU];
-        // codes and scale codes of tile i (page numbers in ids), zeros where there is no slot or page
-        auto load = [&](int32_t i) {
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
-                ks[u] = vs[u] = 127;
-                if (uint32_t(ids[u]) < uint32_t(p.c.num_pages)) {
-                    const uint32_t in = head_at + uint32_t(slot_of(i, u) & (size - 1)) * D;
-                    const int64_t at = int64_t(ids[u]) * page_bytes + in;
-                    kw[u] = __ldg(reinterpret_cast<const uint4 *>(p.c.k + at));
-                    ks[u] = __ldg(p.c.k_scales + (at >> 5));
-                    vw[u] = __ldg(reinterpret_cast<const uint4 *>(p.c.v + at));
-                    vs[u] = __ldg(p.c.v_scales + (at >> 5));
-                }
-            }
-        };
         auto store = [&](uint8_t *dst, const uint4 &w, uint32_t sc, bool values) {
             uint32_t o[8];
             const bool nan = widen16(w, sc, o);
@@ -586,13 +569,27 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 flip ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
         };
         static_assert(kRows % 8 == 0, "a lane's rows swizzle alike");
-#pragma unroll
-        for (int u = 0; u < kU; ++u) ids[u] = entry_of(0, u);
-        load(0);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) ids[u] = entry_of(1, u);
         for (int32_t i = 0; i < sl.ntiles; ++i) {
-            const int st = i % S;
+            const int st = i % S, rs = i % Lay::kRawStages;
+            const uint8_t *raw = smem + Lay::kRaw0 + rs * Lay::kRawBytes;
+            if (!mbar_wait(&sb.raw_full[rs], (i / Lay::kRawStages) & 1, abort)) break;
+            const uint32_t there = sb.there[i % 16];
+            uint4 kw[kU], vw[kU];
+            uint32_t ks[kU], vs[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int r = r0 + kRows * u;
+                kw[u] = *reinterpret_cast<const uint4 *>(raw + r * D + col * 16);
+                vw[u] = *reinterpret_cast<const uint4 *>(raw + Lay::kRawV + r * D + col * 16);
+                ks[u] = raw[Lay::kRawKs + r * (D / 32) + col / 2];
+                vs[u] = raw[Lay::kRawVs + r * (D / 32) + col / 2];
+                if ((r & 15) >= int((there >> (8 * (r >> 4))) & 0xffu)) { // no such slot: zeros
+                    kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    ks[u] = vs[u] = 127;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.raw_empty[rs]);
             if (!mbar_wait(&sb.empty[st], ((i / S) & 1) ^ 1, abort)) break;
             uint8_t *dst = chunk + 2 * st * Lay::kTileBytes;
 #pragma unroll
@@ -603,10 +600,54 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.full[st]);
-            load(i + 1);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) ids[u] = entry_of(i + 2, u);
         }
+    } else if (warp == kCopyWarp) {
+        warpgroup_regs_dec<kRegsMma>();
+        // ------------------------------------------------- bulk copies ---
+        // lane 4 x + y copies array y (K, V, their scales) of piece x: a page's slots of this
+        // head, or the half of a 128-slot page that the tile covers
+        const int32_t slots = min(size, kKeys), piece = lane >> 2, array = lane & 3;
+        const bool mine = piece < kKeys / slots;
+        const uint8_t *const src = array == 0 ? p.c.k : array == 1 ? p.c.v : array == 2 ? p.c.k_scales : p.c.v_scales;
+        const uint32_t row_bytes = array < 2 ? D : D / 32;
+        const uint32_t offset = (array == 0 ? 0 : array == 1 ? Lay::kRawV : array == 2 ? Lay::kRawKs : Lay::kRawVs) +
+                                piece * slots * row_bytes;
+        auto slot_of = [&](int32_t i) { return sl.listed ? unit_slot(sl, sb, i, piece) : sl.from + i * kKeys + piece * slots; };
+        auto entry_of = [&](int32_t i) -> int32_t { // page table entry, not checked yet
+            if (!mine || i >= sl.ntiles) return -1;
+            const int32_t us = slot_of(i);
+            return us < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (us >> p.c.page_shift)) : -1;
+        };
+        int32_t next = entry_of(0), i = 0;
+        for (; i < sl.ntiles; ++i) {
+            const int rs = i % Lay::kRawStages;
+            const int32_t id = next;
+            next = entry_of(i + 1);
+            int32_t count = 0; // slots of the piece that there are
+            const int32_t us = slot_of(i);
+            if (uint32_t(id) < uint32_t(p.c.num_pages)) count = min(sl.end - us, slots);
+            else if (mine && us < sl.end) cache_range_error(p.c);
+            uint32_t there = 0;
+            if (mine && array == 0)
+                for (int32_t g = 0; g < slots / 16; ++g)
+                    there |= uint32_t(max(0, min(16, count - 16 * g))) << (8 * (piece * (slots / 16) + g));
+            there = __reduce_or_sync(0xffffffffu, there);
+            const uint32_t bytes = count > 0 ? slots * row_bytes : 0;
+            const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+            if (!mbar_wait(&sb.raw_empty[rs], ((i / Lay::kRawStages) & 1) ^ 1, abort)) break;
+            if (lane == 0) {
+                sb.there[i % 16] = there;
+                mbar_arrive_expect_tx(&sb.raw_full[rs], total);
+            }
+            __syncwarp();
+            if (bytes)
+                bulk_load(smem + Lay::kRaw0 + rs * Lay::kRawBytes + offset,
+                          src + cache_row(p.c, id, h, us & (size - 1)) * row_bytes, bytes, &sb.raw_full[rs]);
+        }
+        // no copy may be under way when the block ends (after a timed-out wait, too)
+        int late = 0;
+        for (int32_t j = max(0, i - Lay::kRawStages); j < i; ++j)
+            mbar_wait(&sb.raw_full[j % Lay::kRawStages], (j / Lay::kRawStages) & 1, &late);
     } else {
         warpgroup_regs_dec<kRegsMma>();
         // ---------------------------------------------------- MMA issue ---
