@@ -725,7 +725,8 @@ class HistoryCache:
     copied: the caller changes page_table in place as histories grow.
     """
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "page_table", "status", "struct", "_ref", "batch", "device")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "page_table", "status", "struct", "batch", "device", "_ref",
+                 "_index", "_row", "_words")
 
     def __init__(self, k, v, k_scales, v_scales, page_table, status=None):
         if k.dim() != 4:
@@ -752,7 +753,8 @@ class HistoryCache:
         self.struct = BACache(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                               page_table.data_ptr(), status.data_ptr(), page_table.shape[0], page_table.shape[1],
                               num_pages, page_size, kv_heads, head_dim)
-        self._ref = ctypes.byref(self.struct)
+        self._ref, self._index = ctypes.byref(self.struct), k.get_device()
+        self._row, self._words = (kv_heads, head_dim), (page_table.shape[1] + 31) // 32
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, page_table):
@@ -808,33 +810,45 @@ def ba_cache_fwd(cache, problem, q, q_offsets, lens, positions, tree_mask, tree_
                                     _stream(stream)))
 
 
-def _check_cache_args(cache, named):
-    """(name, tensor, dtype, shape) of each argument: contiguous, on the cache's device, which is the current one
-    (the library launches on the current device)."""
-    dev = cache.device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}: make it the current device")
+def _fits(cache, t, dtype, shape) -> bool:
+    """A contiguous tensor of this type and shape on the cache's device."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == cache._index and t.is_contiguous()
+
+
+def _refuse(cache, named):
+    """The ValueError for the first of (name, tensor, dtype, shape) that does not fit."""
     for name, t, dtype, shape in named:
-        if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
+        if not _fits(cache, t, dtype, shape):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {cache.device}")
+    raise ValueError(f"the cache is on {cache.device}: make it the current device")
 
 
-def _cache_rows(cache, k, v, row_offsets, starts):
-    if k.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {k.dtype}")
-    s = cache.struct
-    shape = (k.shape[0], s.kv_heads, s.head_dim)
-    _check_cache_args(cache, (("k", k, k.dtype, shape), ("v", v, k.dtype, shape),
-                              ("row_offsets", row_offsets, torch.int32, (s.batch + 1,)),
-                              ("starts", starts, torch.int32, (s.batch,))))
+def _on(cache, stream):
+    """The stream to launch on; the library launches on the current device, which must be the cache's."""
+    if torch._C._cuda_getDevice() != cache._index:
+        _refuse(cache, ())
+    # (a stream is a few attribute look-ups away in torch.cuda; a step of small calls feels them)
+    return torch._C._cuda_getCurrentRawStream(cache._index) if stream is None else _stream(stream)
+
+
+def _check_rows(cache, k, v, row_offsets, starts):
+    dtype = k.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    rows, b = (k.shape[0], *cache._row), cache.batch
+    if not (_fits(cache, k, dtype, rows) and _fits(cache, v, dtype, rows)
+            and _fits(cache, row_offsets, torch.int32, (b + 1,)) and _fits(cache, starts, torch.int32, (b,))):
+        _refuse(cache, (("k", k, dtype, rows), ("v", v, dtype, rows),
+                        ("row_offsets", row_offsets, torch.int32, (b + 1,)), ("starts", starts, torch.int32, (b,))))
 
 
 def cache_write(cache, k, v, row_offsets, starts, stream=None):
     """Quantises the jagged rows of k and v [rows, kv_heads, head_dim] (bf16 or
     float32) into the cache: row t of sequence b goes to slot starts[b] + t
     (ba_cache_write)."""
-    _cache_rows(cache, k, v, row_offsets, starts)
-    st = ba_cache_write(cache, _DTYPES[k.dtype], k, v, row_offsets, starts, k.shape[0], stream)
+    _check_rows(cache, k, v, row_offsets, starts)
+    st = _load().ba_cache_write(cache._ref, _DTYPES[k.dtype], k.data_ptr(), v.data_ptr(), row_offsets.data_ptr(),
+                                starts.data_ptr(), k.shape[0], _on(cache, stream))
     if st != BA_OK:
         raise BAError(st, "ba_cache_write")
 
@@ -846,12 +860,12 @@ def cache_read(cache, row_offsets, starts, total_rows, dtype=torch.bfloat16, k=N
     if (k is None) != (v is None):
         raise ValueError("pass both k and v, or neither")
     if k is None:
-        s = cache.struct
-        k, v = (torch.empty((total_rows, s.kv_heads, s.head_dim), dtype=dtype, device=cache.device) for _ in "kv")
-    _cache_rows(cache, k, v, row_offsets, starts)
+        k, v = (torch.empty((total_rows, *cache._row), dtype=dtype, device=cache.device) for _ in "kv")
+    _check_rows(cache, k, v, row_offsets, starts)
     if k.shape[0] != total_rows:
         raise ValueError(f"k and v must have {total_rows} rows")
-    st = ba_cache_read(cache, _DTYPES[k.dtype], row_offsets, starts, total_rows, k, v, stream)
+    st = _load().ba_cache_read(cache._ref, _DTYPES[k.dtype], row_offsets.data_ptr(), starts.data_ptr(), total_rows,
+                               k.data_ptr(), v.data_ptr(), _on(cache, stream))
     if st != BA_OK:
         raise BAError(st, "ba_cache_read")
     return k, v
@@ -860,25 +874,31 @@ def cache_read(cache, row_offsets, starts, total_rows, dtype=torch.bfloat16, k=N
 def cache_summarize(cache, starts, ends, summaries, stream=None):
     """Mean keys of the full pages that hold a slot in [starts[b], ends[b]) into
     summaries, float32 [num_pages, kv_heads, head_dim] (ba_cache_summarize)."""
-    s = cache.struct
-    _check_cache_args(cache, (("starts", starts, torch.int32, (s.batch,)), ("ends", ends, torch.int32, (s.batch,)),
-                              ("summaries", summaries, torch.float32, (s.num_pages, s.kv_heads, s.head_dim))))
-    st = ba_cache_summarize(cache, starts, ends, summaries, stream)
+    b, shape = (cache.batch,), (cache.struct.num_pages, *cache._row)
+    if not (_fits(cache, starts, torch.int32, b) and _fits(cache, ends, torch.int32, b)
+            and _fits(cache, summaries, torch.float32, shape)):
+        _refuse(cache, (("starts", starts, torch.int32, b), ("ends", ends, torch.int32, b),
+                        ("summaries", summaries, torch.float32, shape)))
+    st = _load().ba_cache_summarize(cache._ref, starts.data_ptr(), ends.data_ptr(), summaries.data_ptr(),
+                                    _on(cache, stream))
     if st != BA_OK:
         raise BAError(st, "ba_cache_summarize")
     return summaries
 
 
 def _check_queries(cache, q, q_offsets, lens, positions):
-    s = cache.struct
-    if q.dim() != 3 or q.shape[1] % s.kv_heads:
+    """The queries' problem, after their checks."""
+    if q.dim() != 3 or q.shape[1] % cache._row[0]:
         raise ValueError("q must be [rows, heads, head_dim] with heads a multiple of the cache's kv_heads")
-    rows = q.shape[0]
-    named = [("q", q, torch.bfloat16, (rows, q.shape[1], s.head_dim)),
-             ("q_offsets", q_offsets, torch.int32, (s.batch + 1,)), ("lens", lens, torch.int32, (s.batch,))]
-    if positions is not None:
-        named.append(("positions", positions, torch.int32, (rows,)))
-    return rows, named
+    rows, heads, _ = q.shape
+    b, shape = cache.batch, (rows, heads, cache._row[1])
+    if not (_fits(cache, q, torch.bfloat16, shape) and _fits(cache, q_offsets, torch.int32, (b + 1,))
+            and _fits(cache, lens, torch.int32, (b,))
+            and (positions is None or _fits(cache, positions, torch.int32, (rows,)))):
+        named = [("q", q, torch.bfloat16, shape), ("q_offsets", q_offsets, torch.int32, (b + 1,)),
+                 ("lens", lens, torch.int32, (b,))]
+        _refuse(cache, named if positions is None else [*named, ("positions", positions, torch.int32, (rows,))])
+    return BAProblem(b, rows, heads, shape[2], BA_BF16)
 
 
 def cache_select(cache, q, q_offsets, lens, summaries, block, window, topk, positions=None, page_mask=None,
@@ -886,16 +906,16 @@ def cache_select(cache, q, q_offsets, lens, summaries, block, window, topk, posi
     """The topk pages outside each query's window whose mean keys score highest,
     as bits, int32 [rows, kv_heads, ceil(max_pages / 32)] (ba_cache_select);
     allocates page_mask with torch."""
-    s = cache.struct
-    rows, named = _check_queries(cache, q, q_offsets, lens, positions)
-    words = (s.max_pages + 31) // 32
+    prob = _check_queries(cache, q, q_offsets, lens, positions)
+    kv_heads = cache._row[0]
+    words, means = (prob.total_tokens, kv_heads, cache._words), (cache.struct.num_pages, *cache._row)
     if page_mask is None:
-        page_mask = torch.empty((rows, s.kv_heads, words), dtype=torch.int32, device=cache.device)
-    named += [("summaries", summaries, torch.float32, (s.num_pages, s.kv_heads, s.head_dim)),
-              ("page_mask", page_mask, torch.int32, (rows, s.kv_heads, words))]
-    _check_cache_args(cache, named)
-    st = ba_cache_select(cache, make_problem(q, q_offsets), q, q_offsets, lens, positions, summaries, block, window,
-                         topk, page_mask, stream)
+        page_mask = torch.empty(words, dtype=torch.int32, device=cache.device)
+    if not (_fits(cache, summaries, torch.float32, means) and _fits(cache, page_mask, torch.int32, words)):
+        _refuse(cache, (("summaries", summaries, torch.float32, means), ("page_mask", page_mask, torch.int32, words)))
+    st = _load().ba_cache_select(cache._ref, ctypes.byref(prob), q.data_ptr(), q_offsets.data_ptr(), lens.data_ptr(),
+                                 _ptr(positions), summaries.data_ptr(), block, window, topk, page_mask.data_ptr(),
+                                 _on(cache, stream))
     if st != BA_OK:
         raise BAError(st, "ba_cache_select")
     return page_mask
@@ -908,8 +928,13 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
     positions) or candidates, with pages selected outside the window
     (page_mask, from cache_select). Their own keys and values must be in the
     slots from lens on. Allocates out/lse (and a workspace) with torch."""
-    s = cache.struct
-    rows, named = _check_queries(cache, q, q_offsets, lens, positions)
+    prob = _check_queries(cache, q, q_offsets, lens, positions)
+    rows, heads = prob.total_tokens, prob.heads
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((heads, rows), dtype=torch.float32, device=q.device)
+    named = [("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (heads, rows))]
     words = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2:
@@ -917,18 +942,16 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
         words = tree_mask.shape[1]
         named.append(("tree_mask", tree_mask, torch.int32, (rows, words)))
     if page_mask is not None:
-        named.append(("page_mask", page_mask, torch.int32, (rows, s.kv_heads, (s.max_pages + 31) // 32)))
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((q.shape[1], rows), dtype=torch.float32, device=q.device)
-    named += [("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (q.shape[1], rows))]
-    _check_cache_args(cache, named)
-    prob = make_problem(q, q_offsets)
+        named.append(("page_mask", page_mask, torch.int32, (rows, cache._row[0], cache._words)))
+    for _, t, dtype, shape in named:
+        if not _fits(cache, t, dtype, shape):
+            _refuse(cache, named)
+    ref = ctypes.byref(prob)
     if workspace is None:
-        workspace = workspace_for(ba_cache_fwd_workspace_size(cache, prob, block, window), q.device)
-    st = ba_cache_fwd(cache, prob, q, q_offsets, lens, positions, tree_mask, words, page_mask, block, window, out, lse,
-                      workspace, stream=stream)
+        workspace = workspace_for(_load().ba_cache_fwd_workspace_size(cache._ref, ref, block, window), q.device)
+    st = _load().ba_cache_fwd(cache._ref, ref, q.data_ptr(), q_offsets.data_ptr(), lens.data_ptr(), _ptr(positions),
+                              _ptr(tree_mask), words, _ptr(page_mask), block, window, out.data_ptr(), lse.data_ptr(),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _on(cache, stream))
     if st != BA_OK:
         raise BAError(st, "ba_cache_fwd")
     return out, lse

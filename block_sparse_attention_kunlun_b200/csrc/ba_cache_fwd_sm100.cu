@@ -15,12 +15,18 @@
 //
 // Roles of a block (512 threads, two blocks an SM, so that one block's softmax and set-up
 // overlap the other's MMAs):
-//   warps 0-3   softmax: thread t owns row t (TMEM lane t)
+//   warps 0-3   softmax: thread t owns TMEM lane t
 //   warps 4-11  dequantisation of a 64-slot tile
-//   warp 12     MMA issue
-//   warp 13     bulk copies of the tiles' codes (14 and 15 only fill the warpgroup, whose
-//               registers go to the softmax)
+//   warp 14     bulk copies of the tiles' codes
+//   warp 15     MMA issue (on another scheduler than the first softmax warps; 12 and 13 only
+//               fill the warpgroup, whose registers go to the softmax)
 // TMEM columns: O at 0, S at 128 (P over its first 32), Q at 192.
+//
+// S, softmax, P V and the next S follow one another, so the softmax's latency counts. A tile
+// of up to 64 rows leaves half of the 128 lanes empty: Q is then put there again, and the
+// second copy's softmax takes the tile's upper 32 slots (four copies and 16 slots each for
+// up to 32 rows). Each copy has its own running maximum, sum and O, with P zero in the other
+// columns; they are joined like splits when the tile is stored.
 //
 // Columns are kept in the order that widening four codes at once gives, 0 2 1 3 within each
 // four: Q is put in the same order as it is loaded, O is put back as it is stored.
@@ -39,7 +45,7 @@ namespace {
 
 constexpr int kKeys = 64; // slots of a tile
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12, kCopyWarp = 13;
+constexpr int kCopyWarp = 14, kMmaWarp = 15;
 // registers a thread after the split (softmax, dequantisation, MMA warpgroup); two blocks of
 // 512 threads are launched with 64 each: 104 + 2 * 56 + 40 = 4 * 64
 constexpr uint32_t kRegsSoftmax = 104, kRegsDequant = 56, kRegsMma = 40;
@@ -66,11 +72,13 @@ struct MmaShared {
     // per tile (mod 16, more than can be under way): how many slots of each 16 there are, a byte each
     uint32_t there[16];
     uint64_t s_full, p_full, o_final;
+    uint64_t epi_sync;       // barrier of the softmax warps
     uint32_t tmem;
     int abort;
     int32_t min_ws, max_pos; // over the tile's rows
     int32_t nlist;
     int32_t odd_values;      // some value is NaN or infinite
+    float2 ml[kMmaRows];     // each lane's running maximum and sum
     uint32_t wanted[kMmaList / 32 + 1];
     int32_t list[kMmaList];  // first slots of the listed units
 };
@@ -263,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     const int32_t h = blockIdx.y, split = blockIdx.z;
     FwdTile t;
     if (!find_tile(p, kMmaRows, t)) return;
-    const int active = (t.rows + 31) / 32; // softmax warps with rows
+    // copies of the rows among the 128 lanes, and the softmax warps that have any
+    const int copies = t.rows <= 32 ? 4 : (t.rows <= 64 ? 2 : 1), lanes = kMmaRows / copies;
+    const int active = copies > 1 ? 4 : (t.rows + 31) / 32;
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
@@ -275,6 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         mbar_init(&sb.s_full, 1);
         mbar_init(&sb.p_full, active);
         mbar_init(&sb.o_final, 1);
+        mbar_init(&sb.epi_sync, 128);
         sb.abort = 0;
         sb.min_ws = INT32_MAX;
         sb.max_pos = -1;
@@ -294,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     const uint32_t tmem = sb.tmem;
     volatile int *abort = &sb.abort;
 
-    const int32_t row = t.row0 + min(tid, t.rows - 1);
+    const int32_t row = t.row0 + min(tid % lanes, t.rows - 1);
     const RowView rv = row_view(p, t, row); // (warps past the rows: the last row's)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     if (warp < active) {
@@ -375,52 +386,34 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     if (warp < 4) {
         warpgroup_regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------ softmax ---
-        if (warp < active) {
-        const bool valid = tid < t.rows;
         const uint32_t s_addr = tmem + lane_base + Lay::kColS, o_addr = tmem + lane_base + Lay::kColO;
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int32_t i = 0; i < sl.ntiles; ++i) {
-            uint64_t bits = 0;
-            if (!sl.listed) {
-                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end);
+        // one tile's W columns from column W * copy on
+        auto softmax_tile = [&](int32_t i, uint64_t bits, auto width) {
+            constexpr int W = decltype(width)::value;
+            const int c0 = W == kKeys ? 0 : tid / lanes * W;
+            uint32_t sr[W];
+            if constexpr (W == 16) {
+                tmem_ld16(s_addr + c0, sr);
             } else {
-                for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
-                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end)
-                            << (k << sl.shift);
-            }
-            // slots whose page has no number are unseen
-            if (!mbar_wait(&sb.full[i % S], (i / S) & 1, abort)) {
-                ok = false;
-                break;
-            }
-            const uint32_t there = sb.there[i % 16];
-            if (there != 0x10101010u)
-                for (int g = 0; g < 4; ++g)
-                    if (((there >> (8 * g)) & 0xffu) == 0) bits &= ~(uint64_t(0xffff) << (16 * g));
-            const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
-            const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
-            if (!mbar_wait(&sb.s_full, i & 1, abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t sr[2][32];
-            tmem_ld32(s_addr, sr[0]);
-            tmem_ld32(s_addr + 32, sr[1]);
-            tmem_wait_ld();
-            reg_fence(sr[0]);
-            reg_fence(sr[1]);
-            if (!full) {
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    sr[c / 32][c % 32] = (vis[c / 32] & (1u << (c % 32))) ? sr[c / 32][c % 32] : 0xff800000u;
+                for (int c = 0; c < W; c += 32) tmem_ld32(s_addr + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(sr + c));
+            }
+            tmem_wait_ld();
+            reg_fence(sr);
+            bits >>= c0;
+            const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
+            const uint32_t all = W == 16 ? 0xffffu : 0xffffffffu;
+            const bool full = (vis[0] & all) == all && (W < kKeys || vis[1] == all);
+            if (!__all_sync(0xffffffffu, full)) {
+#pragma unroll
+                for (int c = 0; c < W; ++c) sr[c] = (vis[c / 32] & (1u << (c % 32))) ? sr[c] : 0xff800000u;
             }
             float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 2)
-                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], __uint_as_float(sr[c / 32][c % 32]),
-                                        __uint_as_float(sr[c / 32][c % 32 + 1]));
+            for (int c = 0; c < W; c += 2)
+                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
             const float m_new = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
             // O and l move to the new maximum only when it grew by more than 2^8
             float alpha = 1.f;
@@ -432,17 +425,28 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
             float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            uint32_t pk[32];
+            uint32_t pk[W / 2];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float2 x = ffma2(make_float2(__uint_as_float(sr[c / 16][2 * (c % 16)]),
-                                                   __uint_as_float(sr[c / 16][2 * (c % 16) + 1])),
-                                       sc2, nm2);
+            for (int c = 0; c < W / 2; ++c) {
+                const float2 x =
+                    ffma2(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2);
                 const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
                 acc[c % 2] = fadd2(acc[c % 2], make_float2(p0, p1));
                 pk[c] = pack_bf16x2(p0, p1);
             }
-            tmem_st32(s_addr, pk);
+            // P, zero in the other copies' columns
+            if constexpr (W == kKeys) {
+                tmem_st32(s_addr, pk);
+            } else if constexpr (W == 32) {
+                const uint32_t zero[16] = {};
+                tmem_st16(s_addr + c0 / 2, pk);
+                tmem_st16(s_addr + 16 - c0 / 2, zero);
+            } else {
+                const uint32_t zero[8] = {};
+                tmem_st8(s_addr + c0 / 2, pk);
+#pragma unroll
+                for (int x = 1; x < 4; ++x) tmem_st8(s_addr + (c0 / 2 + 8 * x) % 32, zero);
+            }
             const float2 sum = fadd2(acc[0], acc[1]);
             l = fmaf(l, alpha, sum.x + sum.y);
             // O holds the earlier tiles' P V (complete: this S was issued after it)
@@ -459,13 +463,51 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 }
             }
             tmem_wait_st();
+        };
+        for (int32_t i = 0; warp < active && i < sl.ntiles; ++i) {
+            uint64_t bits = 0;
+            if (!sl.listed) {
+                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end);
+            } else {
+                for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
+                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end) << (k << sl.shift);
+            }
+            // slots whose page has no number are unseen
+            if (!mbar_wait(&sb.full[i % S], (i / S) & 1, abort)) {
+                ok = false;
+                break;
+            }
+            const uint32_t there = sb.there[i % 16];
+            if (there != 0x10101010u)
+                for (int g = 0; g < 4; ++g)
+                    if (((there >> (8 * g)) & 0xffu) == 0) bits &= ~(uint64_t(0xffff) << (16 * g));
+            if (!mbar_wait(&sb.s_full, i & 1, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (copies == 4) softmax_tile(i, bits, std::integral_constant<int, 16>{});
+            else if (copies == 2) softmax_tile(i, bits, std::integral_constant<int, 32>{});
+            else softmax_tile(i, bits, std::integral_constant<int, 64>{});
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.p_full);
         }
-        if (ok && sl.ntiles > 0) ok = mbar_wait(&sb.o_final, 0, abort);
-        if (ok) {
+        // ----------------------------------------------------- epilogue ---
+        // the lanes' O, each at the maximum over its row's copies, through shared memory (the
+        // tiles are no longer needed: the last P V is complete) to rows written by whole warps
+        uint32_t phase = 0;
+        sb.ml[tid] = make_float2(m_ref, l);
+        if (ok && warp < active && sl.ntiles > 0) ok = mbar_wait(&sb.o_final, 0, abort);
+        ok = group_sync(&sb.epi_sync, phase, abort) && ok;
+        constexpr int kStride = D + 4; // floats a row, so that lanes' rows start in different banks
+        static_assert(kMmaRows * kStride * 4 <= Lay::kBytes, "staged O fits");
+        float *const stage = reinterpret_cast<float *>(smem);
+        if (ok && warp < active) {
             tc_fence_after();
+            float top = m_ref;
+            for (int x = 1; x < copies; ++x) top = fmaxf(top, sb.ml[(tid + x * lanes) % kMmaRows].x);
+            const float f = l == 0.f ? 0.f : ex2_approx(m_ref - top);
             OddValues<D> odd;
             const bool any_odd = sl.ntiles > 0 && *reinterpret_cast<volatile int32_t *>(&sb.odd_values);
             if (any_odd) { // (copies: objects whose address is taken would live in memory throughout)
@@ -476,13 +518,6 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 find_odd_values<D>(p, t2, r2, h, s2, sb, o2);
                 odd = o2;
             }
-            const int64_t oh = out_row(p, t, h, row);
-            const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
-            const bool whole = p.nsplit == 1;
-            const int64_t at = whole ? oh : int64_t(split) * p.q.rows * heads + oh;
-            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            // a part without any visible slot is left out by its statistics
-            const bool store = valid && (whole || l != 0.f);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -490,13 +525,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                     tmem_ld32(o_addr + c * 32, o);
                     tmem_wait_ld();
                     reg_fence(o);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0;
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                for (int k = 0; k < 32; ++k) o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) { // 0 2 1 3 back to 0 1 2 3
                     const uint32_t x = o[k + 1];
@@ -513,34 +544,52 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                         if ((odd.nan[c] & b) || (a && n)) o[k] = 0x7fffffffu;
                     }
                 }
-                if (store && whole) {
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + 32 * c);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        dst[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
-                } else if (store) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * c);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                }
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<uint4 *>(stage + tid * kStride + 32 * c + k) =
+                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
             }
-            if (valid) {
-                if (whole) {
-                    const int64_t token = int64_t(t.q0) + row / p.q.group;
-                    p.lse[(int64_t(h) * p.q.group + row % p.q.group) * p.q.rows + token] =
-                        (m_ref + log2f(l)) * 0.6931471805599453f;
+        }
+        ok = group_sync(&sb.epi_sync, phase, abort) && ok;
+        if (ok) {
+            constexpr int C = D / 32; // columns of a lane
+            const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
+            for (int r = warp; r < t.rows; r += 4) {
+                float top = -INFINITY, sum = 0.f, acc[C];
+                for (int x = 0; x < copies; ++x) top = fmaxf(top, sb.ml[r + x * lanes].x);
+#pragma unroll
+                for (int k = 0; k < C; ++k) acc[k] = 0.f;
+                for (int x = 0; x < copies; ++x) {
+                    const float2 ml = sb.ml[r + x * lanes];
+                    sum += ml.y == 0.f ? 0.f : ml.y * ex2_approx(ml.x - top);
+                    const float *src = stage + (r + x * lanes) * kStride + lane * C;
+#pragma unroll
+                    for (int k = 0; k < C; ++k) acc[k] += src[k];
+                }
+                const int64_t oh = out_row(p, t, h, t.row0 + r);
+                if (p.nsplit == 1) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                    for (int k = 0; k < C; k += 2)
+                        *reinterpret_cast<uint32_t *>(p.out + oh * D + lane * C + k) =
+                            pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
+                    if (lane == 0) {
+                        const int64_t token = oh / heads, head = oh % heads;
+                        p.lse[head * p.q.rows + token] = (top + log2f(sum)) * 0.6931471805599453f;
+                    }
                 } else {
-                    p.part_ml[at] = make_float2(m_ref, l);
+                    const int64_t at = int64_t(split) * p.q.rows * heads + oh;
+                    if (sum != 0.f) { // (a part without any visible slot is left out by its statistics)
+#pragma unroll
+                        for (int k = 0; k < C; k += 2)
+                            *reinterpret_cast<float2 *>(p.part_o + at * D + lane * C + k) =
+                                make_float2(acc[k], acc[k + 1]);
+                    }
+                    if (lane == 0) p.part_ml[at] = make_float2(top, sum);
                 }
             }
         }
-        }
-    } else if (warp < kMmaWarp) {
+    } else if (warp < 12) {
         warpgroup_regs_dec<kRegsDequant>();
         // ----------------------------------------------- dequantisation ---
         constexpr int kLanes = D / 16, kRows = 256 / kLanes, kU = kKeys / kRows;
