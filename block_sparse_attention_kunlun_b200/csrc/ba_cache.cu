@@ -52,115 +52,144 @@ __device__ __forceinline__ void load8(const float *x, float (&f)[8])
 
 } // namespace
 
-// Four consecutive lanes hold one 32-value block, eight values each: 16 (or 32) bytes in,
-// 8 bytes out per lane, so a warp reads 512 (1024) and writes 256 consecutive bytes. The
-// block's largest magnitude takes two shuffles; e = floor(log2 amax) - 8 is its exponent
-// field, and multiplying by 2^-e is exact in float32 (the quotient stays below 2^9; what
-// underflows is far below E4M3's smallest value), so the conversion to E4M3 is the only
-// rounding. fmaxf drops NaN: a NaN leaves its block's scale alone and becomes E4M3's NaN;
+// x / d for the head number: by a multiplication with ceil(2^32 / d), exact while x d < 2^32
+// (x < 32 d here), or magic = 0 and a division.
+__device__ __forceinline__ uint32_t div_heads(uint32_t x, uint32_t d, uint32_t magic)
+{
+    return magic ? __umulhi(x, magic) : x / d;
+}
+
+// D / 8 lanes hold a (row, head), eight values each, four lanes one 32-value block: 16 (or 32)
+// bytes in, 8 bytes out per lane, so a warp reads 512 (1024) and writes 256 consecutive bytes
+// of rows and pages. The block's largest magnitude takes two shuffles; e = floor(log2 amax) - 8
+// is its exponent field, and multiplying by 2^-e is exact in float32 (the quotient stays below
+// 2^9; what underflows is far below E4M3's smallest value), so the conversion to E4M3 is the
+// only rounding. fmaxf drops NaN: a NaN leaves its block's scale alone and becomes E4M3's NaN;
 // an infinity gives e = 120 and the largest code.
-template <typename T>
+// Bound by HBM for many rows (each thread has kBatch loads under way), by the launch for few.
+template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_write_kernel(const CacheView c, const T *__restrict__ k, const T *__restrict__ v,
                        const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts, int32_t total_rows,
-                       int32_t rows_per_block)
+                       int32_t rows_per_block, uint32_t magic)
 {
+    constexpr int L = D / 8, kStep = kRowThreads / L, kBatch = 4;
     __shared__ int64_t target[kRowsPerBlock];
     const int32_t row0 = blockIdx.x * rows_per_block;
     const int32_t n = min(rows_per_block, total_rows - row0);
     find_rows(c, row_offsets, starts, row0, n, target);
-    const int32_t D = c.head_dim, per_head = D / 8, per_row = c.kv_heads * per_head;
-    const int32_t units = n * per_row; // lanes of eight values; a multiple of 8 (D >= 64)
     const bool values = blockIdx.y != 0;
-    const T *src = values ? v : k;
+    const int d8 = threadIdx.x % L;
+    const T *src = (values ? v : k) + int64_t(row0) * c.kv_heads * D + d8 * 8;
     uint8_t *elems = values ? c.v : c.k, *scales = values ? c.v_scales : c.k_scales;
-    const int64_t base = int64_t(row0) * per_row;
-    const int32_t head_rows = 1 << c.page_shift;
-#pragma unroll 4
-    for (int32_t u0 = 0; u0 < units; u0 += kRowThreads) {
-        const int32_t u = u0 + threadIdx.x;
-        const bool live = u < units;
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) load8(src + (base + u) * 8, f);
-        float amax = fmaxf(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))),
-                           fmaxf(fmaxf(fabsf(f[4]), fabsf(f[5])), fmaxf(fabsf(f[6]), fabsf(f[7]))));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const uint32_t bits = __float_as_uint(amax);
-        // exponent code e + 127 = field - 8, not below 0 (subnormal maxima too); an all-zero block has e = -8
-        uint32_t code = bits >> 23;
-        code = amax > 0.f ? (code > 8 ? code - 8 : 0u) : 119u;
-        const float inv = __uint_as_float(code < 254 ? (254 - code) << 23 : 0x00400000u);
-        uint32_t w[2];
+    const uint32_t heads = c.kv_heads, all = n * heads;
+    for (uint32_t x0 = 0; x0 < all; x0 += kBatch * kStep) {
+        float f[kBatch][8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i] * inv, f[4 * i + 1] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2] * inv, f[4 * i + 3] * inv),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | (hi << 16);
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t x = x0 + i * kStep + threadIdx.x / L;
+            if (x < all) {
+                load8(src + int64_t(x) * D, f[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+            }
         }
-        const int32_t r = u / per_row, x = u % per_row, h = x / per_head, d8 = x % per_head;
-        // the head's scale codes as one word (two or four bytes), gathered by its first lane
-        uint32_t word = code << (8 * (d8 / 4));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        if (D == 128) word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        if (!live || target[r] < 0) continue;
-        const int64_t row = target[r] + int64_t(h) * head_rows;
-        *reinterpret_cast<uint2 *>(elems + row * D + d8 * 8) = make_uint2(w[0], w[1]);
-        if (d8 == 0) {
-            if (D == 128) *reinterpret_cast<uint32_t *>(scales + row * 4) = word;
-            else *reinterpret_cast<uint16_t *>(scales + row * 2) = uint16_t(word);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t x = x0 + i * kStep + threadIdx.x / L;
+            float amax = fmaxf(fmaxf(fmaxf(fabsf(f[i][0]), fabsf(f[i][1])), fmaxf(fabsf(f[i][2]), fabsf(f[i][3]))),
+                               fmaxf(fmaxf(fabsf(f[i][4]), fabsf(f[i][5])), fmaxf(fabsf(f[i][6]), fabsf(f[i][7]))));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // exponent code e + 127 = field - 8, not below 0 (subnormal maxima too); an all-zero block has e = -8
+            uint32_t code = __float_as_uint(amax) >> 23;
+            code = amax > 0.f ? (code > 8 ? code - 8 : 0u) : 119u;
+            const float inv = __uint_as_float(code < 254 ? (254 - code) << 23 : 0x00400000u);
+            uint32_t w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float *g = f[i] + 4 * j;
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(g[0] * inv, g[1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(g[2] * inv, g[3] * inv), __NV_SATFINITE, __NV_E4M3);
+                w[j] = lo | (hi << 16);
+            }
+            // the head's scale codes as one word (two or four bytes), gathered by its first lane
+            uint32_t word = code << (8 * (d8 / 4));
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            if (D == 128) word |= __shfl_xor_sync(0xffffffffu, word, 8);
+            if (x >= all) continue;
+            const uint32_t r = div_heads(x, heads, magic), h = x - r * heads;
+            if (target[r] < 0) continue;
+            const int64_t row = target[r] + (int64_t(h) << c.page_shift);
+            *reinterpret_cast<uint2 *>(elems + row * D + d8 * 8) = make_uint2(w[0], w[1]);
+            if (d8 == 0) {
+                if (D == 128) *reinterpret_cast<uint32_t *>(scales + row * 4) = word;
+                else *reinterpret_cast<uint16_t *>(scales + row * 2) = uint16_t(word);
+            }
         }
     }
 }
 
-// Sixteen values a lane: 16 bytes of codes in, 32 (bf16) or 64 bytes out. A bf16 result is
-// exact (four significant bits) unless it falls below bf16's normal range.
-template <typename T>
+// D / 16 lanes hold a (row, head), sixteen values each: 16 bytes of codes in, 32 (bf16) or 64
+// bytes out. A bf16 result is exact (four significant bits) unless it falls below bf16's
+// normal range. Bound by HBM.
+template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_read_kernel(const CacheView c, const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts,
-                      int32_t total_rows, int32_t rows_per_block, T *__restrict__ k, T *__restrict__ v)
+                      int32_t total_rows, int32_t rows_per_block, uint32_t magic, T *__restrict__ k, T *__restrict__ v)
 {
+    constexpr int L = D / 16, kStep = kRowThreads / L, kBatch = 2;
     __shared__ int64_t target[kRowsPerBlock];
     const int32_t row0 = blockIdx.x * rows_per_block;
     const int32_t n = min(rows_per_block, total_rows - row0);
     find_rows(c, row_offsets, starts, row0, n, target);
-    const int32_t D = c.head_dim, per_head = D / 16, per_row = c.kv_heads * per_head;
-    const int32_t units = n * per_row;
     const bool values = blockIdx.y != 0;
-    T *dst = values ? v : k;
+    const int d16 = threadIdx.x % L;
+    T *dst = (values ? v : k) + int64_t(row0) * c.kv_heads * D + d16 * 16;
     const uint8_t *elems = values ? c.v : c.k, *scales = values ? c.v_scales : c.k_scales;
-    const int64_t base = int64_t(row0) * per_row;
-    const int32_t head_rows = 1 << c.page_shift;
-#pragma unroll 4
-    for (int32_t u = threadIdx.x; u < units; u += kRowThreads) {
-        const int32_t r = u / per_row, x = u % per_row, h = x / per_head, d16 = x % per_head;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        float s = 0.f;
-        if (target[r] >= 0) {
-            const int64_t row = target[r] + int64_t(h) * head_rows;
-            w = __ldg(reinterpret_cast<const uint4 *>(elems + row * D) + d16);
-            s = mx_scale(__ldg(scales + row * (D / 32) + d16 / 2));
-        }
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        uint32_t o[16];
+    const uint32_t heads = c.kv_heads, all = n * heads;
+    for (uint32_t x0 = threadIdx.x / L; x0 < all; x0 += kBatch * kStep) {
+        uint4 w[kBatch];
+        uint32_t code[kBatch];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
-            f.x *= s;
-            f.y *= s;
-            if (sizeof(T) == 2) {
-                o[i] = pack_bf16x2(f.x, f.y);
-            } else {
-                o[2 * i] = __float_as_uint(f.x);
-                o[2 * i + 1] = __float_as_uint(f.y);
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t x = x0 + i * kStep;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            code[i] = 127;
+            if (x < all) {
+                const uint32_t r = div_heads(x, heads, magic), h = x - r * heads;
+                if (target[r] >= 0) {
+                    const int64_t row = target[r] + (int64_t(h) << c.page_shift);
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(elems + row * D) + d16);
+                    code[i] = __ldg(scales + row * (D / 32) + d16 / 2);
+                }
             }
         }
-        uint4 *out = reinterpret_cast<uint4 *>(dst + (base + u) * 16);
 #pragma unroll
-        for (int i = 0; i < int(sizeof(T)); ++i)
-            __stcs(out + i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t x = x0 + i * kStep;
+            if (x >= all) break;
+            const float s = mx_scale(code[i]);
+            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[4 * sizeof(T)];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 f = e4m3x2_to_f32((ws[j / 2] >> (16 * (j % 2))) & 0xffffu);
+                f.x *= s;
+                f.y *= s;
+                if constexpr (sizeof(T) == 2) {
+                    o[j] = pack_bf16x2(f.x, f.y);
+                } else {
+                    o[2 * j] = __float_as_uint(f.x);
+                    o[2 * j + 1] = __float_as_uint(f.y);
+                }
+            }
+            uint4 *out = reinterpret_cast<uint4 *>(dst + int64_t(x) * D);
+#pragma unroll
+            for (int j = 0; j < int(sizeof(T)); ++j)
+                __stcs(out + j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+        }
     }
 }
 
@@ -176,19 +205,41 @@ int32_t rows_per_block(int32_t total_rows, int num_sms)
 
 } // namespace
 
+namespace {
+
+uint32_t heads_magic(int32_t heads)
+{
+    return heads > 1 && heads <= 8192 ? uint32_t(((uint64_t(1) << 32) + heads - 1) / heads) : 0;
+}
+
+template <typename T, int D>
+void launch_write(const CacheView &c, const void *k, const void *v, const int32_t *row_offsets, const int32_t *starts,
+                  int32_t total_rows, int32_t rpb, cudaStream_t stream)
+{
+    cache_write_kernel<T, D><<<dim3((total_rows + rpb - 1) / rpb, 2), kRowThreads, 0, stream>>>(
+        c, static_cast<const T *>(k), static_cast<const T *>(v), row_offsets, starts, total_rows, rpb,
+        heads_magic(c.kv_heads));
+}
+
+template <typename T, int D>
+void launch_read(const CacheView &c, const int32_t *row_offsets, const int32_t *starts, int32_t total_rows, void *k,
+                 void *v, int32_t rpb, cudaStream_t stream)
+{
+    cache_read_kernel<T, D><<<dim3((total_rows + rpb - 1) / rpb, 2), kRowThreads, 0, stream>>>(
+        c, row_offsets, starts, total_rows, rpb, heads_magic(c.kv_heads), static_cast<T *>(k), static_cast<T *>(v));
+}
+
+} // namespace
+
 cudaError_t launch_cache_write(const CacheView &c, bool f32, const void *k, const void *v, const int32_t *row_offsets,
                                const int32_t *starts, int32_t total_rows, int num_sms, cudaStream_t stream)
 {
     const int32_t rpb = rows_per_block(total_rows, num_sms);
-    const dim3 grid((total_rows + rpb - 1) / rpb, 2);
-    if (f32)
-        cache_write_kernel<float><<<grid, kRowThreads, 0, stream>>>(c, static_cast<const float *>(k),
-                                                                    static_cast<const float *>(v), row_offsets, starts,
-                                                                    total_rows, rpb);
-    else
-        cache_write_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(
-            c, static_cast<const __nv_bfloat16 *>(k), static_cast<const __nv_bfloat16 *>(v), row_offsets, starts,
-            total_rows, rpb);
+    if (f32 && c.head_dim == 64) launch_write<float, 64>(c, k, v, row_offsets, starts, total_rows, rpb, stream);
+    else if (f32) launch_write<float, 128>(c, k, v, row_offsets, starts, total_rows, rpb, stream);
+    else if (c.head_dim == 64)
+        launch_write<__nv_bfloat16, 64>(c, k, v, row_offsets, starts, total_rows, rpb, stream);
+    else launch_write<__nv_bfloat16, 128>(c, k, v, row_offsets, starts, total_rows, rpb, stream);
     return cudaGetLastError();
 }
 
@@ -196,36 +247,36 @@ cudaError_t launch_cache_read(const CacheView &c, bool f32, const int32_t *row_o
                               int32_t total_rows, void *k, void *v, int num_sms, cudaStream_t stream)
 {
     const int32_t rpb = rows_per_block(total_rows, num_sms);
-    const dim3 grid((total_rows + rpb - 1) / rpb, 2);
-    if (f32)
-        cache_read_kernel<float><<<grid, kRowThreads, 0, stream>>>(c, row_offsets, starts, total_rows, rpb,
-                                                                   static_cast<float *>(k), static_cast<float *>(v));
-    else
-        cache_read_kernel<__nv_bfloat16><<<grid, kRowThreads, 0, stream>>>(c, row_offsets, starts, total_rows, rpb,
-                                                                           static_cast<__nv_bfloat16 *>(k),
-                                                                           static_cast<__nv_bfloat16 *>(v));
+    if (f32 && c.head_dim == 64) launch_read<float, 64>(c, row_offsets, starts, total_rows, k, v, rpb, stream);
+    else if (f32) launch_read<float, 128>(c, row_offsets, starts, total_rows, k, v, rpb, stream);
+    else if (c.head_dim == 64) launch_read<__nv_bfloat16, 64>(c, row_offsets, starts, total_rows, k, v, rpb, stream);
+    else launch_read<__nv_bfloat16, 128>(c, row_offsets, starts, total_rows, k, v, rpb, stream);
     return cudaGetLastError();
 }
 
 // One warp per (page, head): its slots are page_size * head_dim consecutive bytes, read 16
-// bytes a lane; each lane sums its sixteen columns over its rows in float32 and the lanes
-// that share columns are added at the end. Pages first, first + 1, ... of a (sequence,
-// head) are dealt to the warps of gridDim.y blocks.
+// bytes a lane, eight loads at a time; each lane sums its sixteen columns over its rows in
+// float32 and the lanes that share columns are added at the end. The pages of a (sequence,
+// head) are dealt to `share` warps. Bound by HBM for many pages, by one page's latency for few.
 template <int D>
 __global__ void __launch_bounds__(128)
     cache_summarize_kernel(const CacheView c, const int32_t *__restrict__ starts, const int32_t *__restrict__ ends,
-                           float *__restrict__ summaries)
+                           int32_t share, float *__restrict__ summaries)
 {
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes; // lanes of a row, rows of a load
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int32_t b = blockIdx.x / c.kv_heads, h = blockIdx.x % c.kv_heads;
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = 8; // lanes of a row, rows of a load
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int32_t pair = int32_t(unit / share), part = int32_t(unit % share);
+    const int32_t b = pair / c.kv_heads, h = pair % c.kv_heads;
+    if (b >= c.batch) return;
     const int32_t first = max(__ldg(starts + b), 0) >> c.page_shift;
     const int32_t end = max(__ldg(ends + b), 0) >> c.page_shift; // pages below are full
-    if (end > c.max_pages && blockIdx.y == 0 && h == 0 && threadIdx.x == 0) cache_range_error(c);
+    if (end > c.max_pages && part == 0 && h == 0 && lane == 0) cache_range_error(c);
     const int32_t stop = min(end, c.max_pages);
-    const int32_t slots = 1 << c.page_shift;
+    const int32_t loads = (1 << c.page_shift) / kRows; // of a page: 2 .. 32
     const int col = lane % kLanes;
-    for (int32_t pi = first + blockIdx.y * 4 + warp; pi < stop; pi += gridDim.y * 4) {
+    const float inv = 1.f / float(1 << c.page_shift); // a power of two
+    for (int32_t pi = first + part; pi < stop; pi += share) {
         const int32_t id = cache_page(c, b, pi);
         if (id < 0) {
             if (lane == 0) cache_range_error(c);
@@ -234,40 +285,43 @@ __global__ void __launch_bounds__(128)
         const int64_t row0 = cache_row(c, id, h, 0);
         const uint4 *src = reinterpret_cast<const uint4 *>(c.k + row0 * D) + lane;
         const uint8_t *sc = c.k_scales + (row0 + lane / kLanes) * (D / 32) + col / 2;
-        float acc[16];
+        float2 acc[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-        for (int32_t r = 0; r < slots; r += 2 * kRows) { // page_size is a multiple of 16
-            uint4 w[2];
-            float s[2];
+        for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
+        for (int32_t u0 = 0; u0 < loads; u0 += kBatch) {
+            uint4 w[kBatch];
+            uint32_t code[kBatch];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                w[u] = __ldg(src + (r + u * kRows) * kLanes);
-                s[u] = mx_scale(__ldg(sc + (r + u * kRows) * (D / 32)));
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
-                    acc[2 * i] = fmaf(f.x, s[u], acc[2 * i]);
-                    acc[2 * i + 1] = fmaf(f.y, s[u], acc[2 * i + 1]);
+            for (int u = 0; u < kBatch; ++u)
+                if (u0 + u < loads) {
+                    w[u] = __ldg(src + (u0 + u) * 32);
+                    code[u] = __ldg(sc + (u0 + u) * kRows * (D / 32));
                 }
-            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u0 + u < loads) {
+                    const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                    const float s = mx_scale(code[u]);
+                    const float2 s2 = make_float2(s, s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        acc[i] = ffma2(e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), s2, acc[i]);
+                }
         }
-        const float inv = 1.f / float(slots); // a power of two
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
 #pragma unroll
-            for (int m = kLanes; m < 32; m <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
-            acc[i] *= inv;
+            for (int m = kLanes; m < 32; m <<= 1) {
+                acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, m);
+                acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, m);
+            }
         }
         if (lane < kLanes) {
             float4 *dst = reinterpret_cast<float4 *>(summaries + (int64_t(id) * c.kv_heads + h) * D) + col * 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                dst[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                dst[i] = make_float4(acc[2 * i].x * inv, acc[2 * i].y * inv, acc[2 * i + 1].x * inv,
+                                     acc[2 * i + 1].y * inv);
         }
     }
 }
@@ -275,12 +329,15 @@ __global__ void __launch_bounds__(128)
 cudaError_t launch_cache_summarize(const CacheView &c, const int32_t *starts, const int32_t *ends, float *summaries,
                                    int num_sms, cudaStream_t stream)
 {
+    // enough warps to fill the GPU whatever the number of (sequence, head) pairs
     const int64_t pairs = int64_t(c.batch) * c.kv_heads;
-    int64_t x = (int64_t(num_sms) * 8 + pairs - 1) / pairs, most = (c.max_pages + 3) / 4;
-    if (x > most) x = most;
-    const dim3 grid(unsigned(pairs), unsigned(x < 1 ? 1 : x));
-    if (c.head_dim == 64) cache_summarize_kernel<64><<<grid, 128, 0, stream>>>(c, starts, ends, summaries);
-    else cache_summarize_kernel<128><<<grid, 128, 0, stream>>>(c, starts, ends, summaries);
+    int64_t share = (int64_t(num_sms) * 32 + pairs - 1) / pairs;
+    if (share > c.max_pages) share = c.max_pages;
+    const int64_t blocks = (pairs * share + 3) / 4;
+    if (c.head_dim == 64)
+        cache_summarize_kernel<64><<<unsigned(blocks), 128, 0, stream>>>(c, starts, ends, int32_t(share), summaries);
+    else
+        cache_summarize_kernel<128><<<unsigned(blocks), 128, 0, stream>>>(c, starts, ends, int32_t(share), summaries);
     return cudaGetLastError();
 }
 
@@ -332,7 +389,8 @@ __global__ void __launch_bounds__(256)
                         uint32_t *__restrict__ page_mask)
 {
     constexpr int C = D / 32;                     // columns a lane holds
-    constexpr int kPages = 8 / kRows;             // pages a warp takes at once
+    constexpr int kPages = 8 / kRows;             // pages a warp reduces at once
+    constexpr int kLoads = 8;                     // pages whose means it loads at once
     extern __shared__ uint64_t keys[];            // [kRows][max_pages]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t h = blockIdx.y;
@@ -394,14 +452,14 @@ __global__ void __launch_bounds__(256)
             if (id < 0) cache_range_error(c);
         }
         const int32_t here = min(32, most - p0);
-        for (int32_t j = 0; j < here; j += kPages) {
-            float f[kPages][C];
-            int32_t ids[kPages];
+        for (int32_t j0 = 0; j0 < here; j0 += kLoads) {
+            float f[kLoads][C];
+            int32_t ids[kLoads];
 #pragma unroll
-            for (int u = 0; u < kPages; ++u) {
-                ids[u] = __shfl_sync(0xffffffffu, id, (j + u) & 31);
+            for (int u = 0; u < kLoads; ++u) {
+                ids[u] = __shfl_sync(0xffffffffu, id, (j0 + u) & 31);
                 const float *src = summaries + (int64_t(max(ids[u], 0)) * c.kv_heads + h) * D + lane * C;
-                const bool in = j + u < here;
+                const bool in = j0 + u < here;
                 if constexpr (C == 4) {
                     const float4 x = in ? __ldg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
                     f[u][0] = x.x, f[u][1] = x.y, f[u][2] = x.z, f[u][3] = x.w;
@@ -410,28 +468,32 @@ __global__ void __launch_bounds__(256)
                     f[u][0] = x.x, f[u][1] = x.y;
                 }
             }
-            double part[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int u = kRows == 1 ? i : 0, r = kRows == 1 ? 0 : i;
-                part[i] = 0.0;
+            for (int v = 0; v < kLoads; v += kPages) {
+                if (j0 + v >= here) break;
+                double part[8];
 #pragma unroll
-                for (int x = 0; x < C; ++x) part[i] = fma(qs[r][x], double(f[u][x]), part[i]);
-            }
-            const double s = reduce8(part, lane);
-            if ((lane & 3) == 0) {
-                const int i = ((lane & 16) ? 4 : 0) + ((lane & 8) ? 2 : 0) + ((lane & 4) ? 1 : 0);
-                const int u = kRows == 1 ? i : 0, r = kRows == 1 ? 0 : i;
-                int32_t idu = ids[0], cr = cand[0];
+                for (int i = 0; i < 8; ++i) {
+                    const int u = kRows == 1 ? i : v, r = kRows == 1 ? 0 : i;
+                    part[i] = 0.0;
 #pragma unroll
-                for (int x = 1; x < kPages; ++x)
-                    if (u == x) idu = ids[x];
+                    for (int x = 0; x < C; ++x) part[i] = fma(qs[r][x], double(f[u][x]), part[i]);
+                }
+                const double s = reduce8(part, lane);
+                if ((lane & 3) == 0) {
+                    const int i = ((lane & 16) ? 4 : 0) + ((lane & 8) ? 2 : 0) + ((lane & 4) ? 1 : 0);
+                    const int u = kRows == 1 ? i : v, r = kRows == 1 ? 0 : i;
+                    int32_t idu = ids[kRows == 1 ? 0 : v], cr = cand[0];
 #pragma unroll
-                for (int x = 1; x < kRows; ++x)
-                    if (r == x) cr = cand[x];
-                const int32_t page = p0 + j + u;
-                if (j + u < here)
-                    keys[int64_t(r) * c.max_pages + page] = page < cr && idu >= 0 ? score_key(s) : 0;
+                    for (int x = 1; x < kPages; ++x)
+                        if (u == x) idu = ids[x];
+#pragma unroll
+                    for (int x = 1; x < kRows; ++x)
+                        if (r == x) cr = cand[x];
+                    const int32_t page = p0 + j0 + u;
+                    if (j0 + u < here)
+                        keys[int64_t(r) * c.max_pages + page] = page < cr && idu >= 0 ? score_key(s) : 0;
+                }
             }
         }
     }

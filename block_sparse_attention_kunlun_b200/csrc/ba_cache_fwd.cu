@@ -13,7 +13,8 @@
 // maximum, sum and unnormalised output in float32 and cache_combine_kernel joins them in the
 // order of the splits. Blocks find their sequence themselves: tiles are numbered
 // floor(offs[b] * group / tile_rows) + b, which leaves at least ceil(rows / tile_rows) numbers
-// for every sequence, so no pass over the batch comes first.
+// for every sequence (tiles of one row simply by their row), so no pass over the batch comes
+// first.
 #include "ba_cache_fwd.cuh"
 #include "ba_kernels.cuh"
 #include "ba_ptx.cuh"
@@ -313,7 +314,7 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     const int64_t each = batch > 0 ? (all + batch - 1) / batch : 1;
     plan.tile_rows = each <= 1 ? 1 : (each <= 2 ? 2 : (each <= 4 ? 4 : kMmaRows));
     const bool mma = plan.tile_rows == kMmaRows;
-    plan.tiles = all / plan.tile_rows + batch;
+    plan.tiles = plan.tile_rows > 1 ? all / plan.tile_rows + batch : all;
     // the most slots a tile may meet: the whole cache, or the window and the rows themselves
     int64_t reach = slots;
     if (!has_mask) {

@@ -23,8 +23,8 @@ __device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, 
     int32_t lo = 0, n = p.c.batch;
     while (n > 1) {
         const int32_t step = (n + 31) / 32, at = lo + lane * step;
-        const bool ok =
-            lane * step < n && int64_t(__ldg(offs + at)) * p.q.group / tile_rows + at <= int64_t(blockIdx.x);
+        const bool ok = lane * step < n &&
+                        int64_t(__ldg(offs + at)) * p.q.group / tile_rows + (tile_rows > 1 ? at : 0) <= int64_t(blockIdx.x);
         const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
         n = min(step, n - (cnt - 1) * step);
         lo += (cnt - 1) * step;
@@ -32,7 +32,7 @@ __device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, 
     t.b = lo;
     t.q0 = __ldg(offs + lo);
     t.n = __ldg(offs + lo + 1) - t.q0;
-    const int64_t first = int64_t(t.q0) * p.q.group / tile_rows + lo;
+    const int64_t first = int64_t(t.q0) * p.q.group / tile_rows + (tile_rows > 1 ? lo : 0);
     const int64_t row0 = (int64_t(blockIdx.x) - first) * tile_rows, all = int64_t(t.n) * p.q.group;
     if (row0 >= all) return false;
     t.row0 = int32_t(row0);
