@@ -9,6 +9,8 @@
 #include "ba_kernels.cuh"
 #include "ba_ptx.cuh"
 
+#include <type_traits>
+
 namespace ba {
 
 namespace {
@@ -343,218 +345,335 @@ cudaError_t launch_cache_summarize(const CacheView &c, const int32_t *starts, co
 
 namespace {
 
-// Sum over the warp of eight values a lane: three exchange steps that halve the number of
-// values (each lane keeps the half its bit names), then two plain steps. Afterwards lane l
-// holds the total of value 4 b0 + 2 b1 + b2 of its bits (l & 16, l & 8, l & 4).
-__device__ __forceinline__ double reduce8(double (&x)[8], int lane)
-{
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-        const int m = 16 >> s, half = 4 >> s;
-        const bool up = lane & m;
-#pragma unroll
-        for (int i = 0; i < half; ++i) {
-            const double give = up ? x[i] : x[i + half], keep = up ? x[i + half] : x[i];
-            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-        }
-    }
-    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 2);
-    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-    return x[0];
-}
-
-// A score as a 64-bit number that orders like it; NaN below every number, and 0 is left for
-// pages that are no candidates.
+// Scores as numbers that order like them; NaN below every number, and 0 is left for pages that
+// are no candidates. -0 becomes +0.
 __device__ __forceinline__ uint64_t score_key(double s)
 {
     if (s != s) return 1;
-    const uint64_t b = uint64_t(__double_as_longlong(s + 0.0)); // -0 becomes +0
+    const uint64_t b = uint64_t(__double_as_longlong(s + 0.0));
     return (b >> 63) ? ~b : b | (uint64_t(1) << 63);
 }
+__device__ __forceinline__ uint32_t score_key(float s)
+{
+    if (s != s) return 1;
+    const uint32_t b = __float_as_uint(s + 0.f);
+    return (b >> 31) ? ~b : b | (1u << 31);
+}
+__device__ __forceinline__ float key_score(uint32_t key)
+{
+    return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint32_t warp_min(uint32_t x) { return __reduce_min_sync(0xffffffffu, x); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t x)
+{
+#pragma unroll
+    for (int m = 16; m; m >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+__device__ __forceinline__ uint64_t warp_min(uint64_t x)
+{
+#pragma unroll
+    for (int m = 16; m; m >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+
+// The keys key[0 .. most) of one row as a warp meets them: held in registers (kHeld a lane) or
+// read again each time (kHeld = 0).
+template <typename K, int kHeld>
+struct Keys {
+    const K *key;
+    int32_t most;
+    K held[kHeld > 0 ? kHeld : 1];
+
+    __device__ __forceinline__ Keys(const K *k, int32_t n) : key(k), most(n)
+    {
+        const int lane = threadIdx.x & 31;
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) held[i] = i * 32 + lane < n ? k[i * 32 + lane] : 0;
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        if constexpr (kHeld > 0) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) f(held[i]);
+        } else {
+            for (int32_t p = threadIdx.x & 31; p < most; p += 32) f(key[p]);
+        }
+    }
+    // keys at or above x (x > 0), over the warp
+    __device__ __forceinline__ int32_t count(K x) const
+    {
+        int32_t n = 0;
+        each([&](K y) { n += y >= x; });
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+    // The largest x with at least topk keys at or above it, or any x with exactly topk of them
+    // (count then says topk). The caller has made sure that there are more than topk candidates.
+    // Found bit by bit from the keys' highest differing bit down.
+    __device__ __forceinline__ K edge(int32_t topk, int32_t &count_at) const
+    {
+        constexpr int kTop = sizeof(K) * 8 - 1;
+        K top = 0, low = ~K(0);
+        each([&](K x) {
+            top = max(top, x);
+            low = min(low, x ? x : ~K(0));
+        });
+        top = warp_max(top);
+        low = warp_min(low);
+        const K diff = top ^ low;
+        int bit = sizeof(K) == 8 ? 63 - __clzll((long long)diff) : 31 - __clz(int(diff)); // -1: all alike
+        K x = bit < 0 ? top : bit == kTop ? 0 : top >> (bit + 1) << (bit + 1);             // the common prefix
+        count_at = -1;
+        for (; bit >= 0 && count_at != topk; --bit) {
+            const K trial = x | K(1) << bit;
+            const int32_t n = count(trial);
+            if (n >= topk) {
+                x = trial;
+                count_at = n;
+            }
+        }
+        return x;
+    }
+};
+
+// Bits of the keys above `edge`, and of the first `equal` of those equal to it.
+template <typename K>
+__device__ __forceinline__ void write_bits(const K *key, int32_t most, K edge, int32_t equal, uint32_t *dst,
+                                           int32_t words)
+{
+    const int lane = threadIdx.x & 31;
+    int32_t seen = 0;
+    for (int32_t w = 0; w < words; ++w) {
+        const int32_t p = w * 32 + lane;
+        const K x = p < most ? key[p] : 0;
+        const bool even = x == edge && x != 0;
+        const uint32_t ties = __ballot_sync(0xffffffffu, even);
+        const int32_t rank = seen + __popc(ties & ((1u << lane) - 1));
+        const uint32_t word = __ballot_sync(0xffffffffu, x > edge || (even && rank < equal));
+        seen += __popc(ties);
+        if (lane == 0) dst[w] = word;
+    }
+}
+
+// a warp a row for the final choice, and four for one row's scores
+__host__ __device__ constexpr int select_warps(int rows) { return rows > 4 ? rows : 4; }
+constexpr int kMeanStride = 36; // floats a page in a warp's staged piece: 32 columns, and 4 so that
+                                // eight lanes' 16-byte reads of eight pages meet all banks
 
 } // namespace
 
 // Scores of the candidate pages for kRows rows of one (sequence, key/value head), then the
-// topk of each. Scores are formed in float64: the products of bf16 queries and float32 means
-// are exact there and the sums are off by some 2^-53, so that which of two pages wins does
-// not hang on the order of summation (in float32 some 1 in 10^4 rows would choose another
-// page at its last place). kRows = 1 takes eight pages at a time, kRows = 8 one page for
-// eight rows (each mean read and widened once for them); either way a lane has eight
-// partial sums of D / 32 columns to reduce.
-// The topk-th largest key is found bit by bit from the keys' highest differing bit down:
-// each step counts the keys at or above a trial value. Ties go to the lowest page.
+// topk of each. Which of two pages wins is decided by the scores in float64 (the products of
+// bf16 queries and float32 means are exact there, the sums off by some 2^-53, so the choice
+// does not hang on the order of summation), but few pages need one: all scores are formed in
+// float32, off by at most E = (D + 4) 2^-24 sum |q| max |mean| (D products and additions, the
+// rounding of q's sum over the group; 1.01 for E's own roundings), so with tau the topk-th
+// largest of them, pages above tau + 2 E are in, pages below tau - 2 E out, and only when more
+// than topk pages reach tau - 2 E are those in between scored again in float64. (All in
+// float64: 50 us where this takes less than half; DFMA chains, not bandwidth, were the bound.)
+//
+// A warp takes 32 pages, a lane one of them: 32 columns of their means at a time go through
+// shared memory (read from HBM in whole lines, the next piece's loads under way), and the
+// lane's kRows sums need no exchange with other lanes.
 template <int D, int kRows>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(select_warps(kRows) * 32)
     cache_select_kernel(const CacheView c, const CacheQuery q, const float *__restrict__ summaries, int32_t topk,
                         uint32_t *__restrict__ page_mask)
 {
-    constexpr int C = D / 32;                     // columns a lane holds
-    constexpr int kPages = 8 / kRows;             // pages a warp reduces at once
-    constexpr int kLoads = 8;                     // pages whose means it loads at once
-    extern __shared__ uint64_t keys[];            // [kRows][max_pages]
+    constexpr int kPieces = D / 32, kWarps = select_warps(kRows);
+    extern __shared__ __align__(16) uint64_t keys[]; // [kRows][max_pages]: float32 keys in a row's first half
+    __shared__ __align__(16) float qs[kRows][D];     // the rows' query sums over the group
+    __shared__ __align__(16) float means[kWarps][32 * kMeanStride];
+    __shared__ int32_t cands[kRows];
+    __shared__ uint32_t max_mean;                    // largest |mean| (its bits)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t h = blockIdx.y;
-    // the sequence and its tile of kRows rows: tiles are numbered floor(offs[b] / kRows) + b on
+    // the sequence and its tile of kRows rows: tiles are numbered floor(offs[b] / kRows) + b
+    // (tiles of one row by their row)
     int32_t b, tile;
     {
         int32_t lo = 0, n = c.batch;
         while (n > 1) {
             const int32_t step = (n + 31) / 32, at = lo + lane * step;
-            const bool ok = lane * step < n && __ldg(q.q_offsets + at) / kRows + at <= int32_t(blockIdx.x);
+            const bool ok = lane * step < n &&
+                            __ldg(q.q_offsets + at) / kRows + (kRows > 1 ? at : 0) <= int32_t(blockIdx.x);
             const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
             n = min(step, n - (cnt - 1) * step);
             lo += (cnt - 1) * step;
         }
         b = lo;
-        tile = int32_t(blockIdx.x) - (__ldg(q.q_offsets + b) / kRows + b);
+        tile = int32_t(blockIdx.x) - (__ldg(q.q_offsets + b) / kRows + (kRows > 1 ? b : 0));
     }
     const int32_t q0 = __ldg(q.q_offsets + b), n = __ldg(q.q_offsets + b + 1) - q0;
     const int32_t t0 = tile * kRows;
     if (t0 >= n) return;
     const int32_t len = max(__ldg(q.lens + b), 0);
     const int32_t full = min(len >> c.page_shift, c.max_pages); // pages below are full
-    // candidates of row t: pages that start before its window and are full
-    int32_t cand[kRows], most = 0;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        cand[r] = 0;
-        if (t0 + r < n) {
-            const int32_t pos = query_position(q, q0, len, t0 + r);
+    if (threadIdx.x < kRows) {
+        // candidates of the row: pages that start before its window and are full
+        int32_t cand = 0;
+        if (t0 + int(threadIdx.x) < n) {
+            const int32_t pos = query_position(q, q0, len, t0 + threadIdx.x);
             const int32_t ws = pos >= 0 ? rule_start(q, pos) : 0;
-            const int32_t before = int32_t((int64_t(ws) + (1 << c.page_shift) - 1) >> c.page_shift);
-            cand[r] = min(before, full);
+            cand = min(int32_t((int64_t(ws) + (1 << c.page_shift) - 1) >> c.page_shift), full);
         }
-        most = max(most, cand[r]);
+        cands[threadIdx.x] = cand;
     }
-    // this lane's columns of the rows' query sums over the group
-    double qs[kRows][C];
+    if (threadIdx.x == 0) max_mean = 0;
+    const __nv_bfloat16 *const q_first = q.q + ((int64_t(q0) + t0) * c.kv_heads + h) * q.group * D;
+    const int64_t q_row = int64_t(c.kv_heads) * q.group * D;
+    // column d of row r's sum over the group
+    auto q_sum = [&](int r, int d) {
+        double s = 0.0;
+        for (int32_t g = 0; g < q.group; ++g) s += double(__bfloat162float(q_first[r * q_row + g * D + d]));
+        return s;
+    };
+    for (int x = threadIdx.x; x < kRows * D; x += kWarps * 32)
+        qs[x / D][x % D] = t0 + x / D < n ? float(q_sum(x / D, x % D)) : 0.f;
+    __syncthreads();
+    int32_t most = 0;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-        for (int i = 0; i < C; ++i) qs[r][i] = 0.0;
-        if (t0 + r < n) {
-            const __nv_bfloat16 *src =
-                q.q + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * q.group * D + lane * C;
-            for (int32_t g = 0; g < q.group; ++g, src += D) {
-#pragma unroll
-                for (int i = 0; i < C; i += 2) {
-                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(src + i));
-                    qs[r][i] += double(f.x);
-                    qs[r][i + 1] += double(f.y);
-                }
-            }
-        }
-    }
-    for (int32_t p0 = warp * 32; p0 < most; p0 += 8 * 32) {
-        int32_t id = 0;
+    for (int r = 0; r < kRows; ++r) most = max(most, cands[r]);
+
+    float *const piece = means[warp];
+    float largest = 0.f;
+    for (int32_t p0 = warp * 32; p0 < most; p0 += kWarps * 32) {
+        int32_t id = -1;
         if (p0 + lane < most) {
             id = cache_page(c, b, p0 + lane);
             if (id < 0) cache_range_error(c);
         }
-        const int32_t here = min(32, most - p0);
-        for (int32_t j0 = 0; j0 < here; j0 += kLoads) {
-            float f[kLoads][C];
-            int32_t ids[kLoads];
+        // lane 8 x + y loads 16 bytes, columns 4 y .. 4 y + 3 of the piece, of pages x, x + 4, ...
+        // (page 0's where there is none: a choice after the load would wait for it here)
+        float4 next[8];
+        uint32_t from[8];
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                ids[u] = __shfl_sync(0xffffffffu, id, (j0 + u) & 31);
-                const float *src = summaries + (int64_t(max(ids[u], 0)) * c.kv_heads + h) * D + lane * C;
-                const bool in = j0 + u < here;
-                if constexpr (C == 4) {
-                    const float4 x = in ? __ldg(reinterpret_cast<const float4 *>(src)) : make_float4(0, 0, 0, 0);
-                    f[u][0] = x.x, f[u][1] = x.y, f[u][2] = x.z, f[u][3] = x.w;
-                } else {
-                    const float2 x = in ? __ldg(reinterpret_cast<const float2 *>(src)) : make_float2(0, 0);
-                    f[u][0] = x.x, f[u][1] = x.y;
-                }
+        for (int u = 0; u < 8; ++u)
+            from[u] = uint32_t(max(__shfl_sync(0xffffffffu, id, 4 * u + (lane >> 3)), 0));
+        const float *const head = summaries + h * D + (lane & 7) * 4;
+        auto load = [&](int part) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                next[u] = __ldg(reinterpret_cast<const float4 *>(head + uint64_t(from[u]) * uint32_t(c.kv_heads * D) +
+                                                                 part * 32));
+        };
+        float here = 0.f; // largest |mean| of this lane's page
+        float2 acc[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) acc[r] = make_float2(0.f, 0.f);
+        load(0);
+#pragma unroll 1
+        for (int part = 0; part < kPieces; ++part) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4 *>(piece + (4 * u + (lane >> 3)) * kMeanStride + 4 * (lane & 7)) = next[u];
+            __syncwarp();
+            if (part + 1 < kPieces) load(part + 1);
+            // a step's operands are read while the previous step's are used
+            float4 m = *reinterpret_cast<const float4 *>(piece + lane * kMeanStride), a[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) a[r] = *reinterpret_cast<const float4 *>(&qs[r][part * 32]);
+#pragma unroll
+            for (int d = 0; d < 32; d += 4) {
+                const int e = (d + 4) % 32;
+                const float4 m2 = *reinterpret_cast<const float4 *>(piece + lane * kMeanStride + e);
+                float4 a2[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) a2[r] = *reinterpret_cast<const float4 *>(&qs[r][part * 32 + e]);
+                here = fmax3(here, fabsf(m.x), fabsf(m.y));
+                here = fmax3(here, fabsf(m.z), fabsf(m.w));
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) acc[r] = ffma2(make_float2(a[r].x, a[r].y), make_float2(m.x, m.y), acc[r]);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) acc[r] = ffma2(make_float2(a[r].z, a[r].w), make_float2(m.z, m.w), acc[r]);
+                m = m2;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) a[r] = a2[r];
             }
+        }
+        if (id >= 0) largest = fmaxf(largest, here);
+        if (p0 + lane < most) {
 #pragma unroll
-            for (int v = 0; v < kLoads; v += kPages) {
-                if (j0 + v >= here) break;
-                double part[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int u = kRows == 1 ? i : v, r = kRows == 1 ? 0 : i;
-                    part[i] = 0.0;
-#pragma unroll
-                    for (int x = 0; x < C; ++x) part[i] = fma(qs[r][x], double(f[u][x]), part[i]);
-                }
-                const double s = reduce8(part, lane);
-                if ((lane & 3) == 0) {
-                    const int i = ((lane & 16) ? 4 : 0) + ((lane & 8) ? 2 : 0) + ((lane & 4) ? 1 : 0);
-                    const int u = kRows == 1 ? i : v, r = kRows == 1 ? 0 : i;
-                    int32_t idu = ids[kRows == 1 ? 0 : v], cr = cand[0];
-#pragma unroll
-                    for (int x = 1; x < kPages; ++x)
-                        if (u == x) idu = ids[x];
-#pragma unroll
-                    for (int x = 1; x < kRows; ++x)
-                        if (r == x) cr = cand[x];
-                    const int32_t page = p0 + j0 + u;
-                    if (j0 + u < here)
-                        keys[int64_t(r) * c.max_pages + page] = page < cr && idu >= 0 ? score_key(s) : 0;
-                }
-            }
+            for (int r = 0; r < kRows; ++r)
+                reinterpret_cast<uint32_t *>(keys + int64_t(r) * c.max_pages)[p0 + lane] =
+                    p0 + lane < cands[r] && id >= 0 ? score_key(acc[r].x + acc[r].y) : 0;
         }
     }
+    const uint32_t most_mean = warp_max(__float_as_uint(largest));
+    if (lane == 0) atomicMax(&max_mean, most_mean);
     __syncthreads();
+
     const int32_t words = (c.max_pages + 31) / 32;
-    for (int32_t r = warp; r < kRows && t0 + r < n; r += 8) {
-        const uint64_t *key = keys + int64_t(r) * c.max_pages;
-        uint32_t *dst = page_mask + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * words;
-        // range of the keys and number of candidates
-        uint64_t top = 0, low = ~uint64_t(0);
-        int32_t live = 0;
-        for (int32_t p = lane; p < most; p += 32) {
-            const uint64_t x = key[p];
-            if (x) {
-                top = max(top, x);
-                low = min(low, x);
-                ++live;
-            }
-        }
+    auto choose = [&](int32_t r, auto held) {
+        constexpr int kHeld = decltype(held)::value;
+        uint64_t *const key64 = keys + int64_t(r) * c.max_pages;
+        uint32_t *const key32 = reinterpret_cast<uint32_t *>(key64);
+        uint32_t *const dst = page_mask + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * words;
+        float bound = 0.f; // sum |q|
+        for (int d = lane; d < D; d += 32) bound += fabsf(qs[r][d]);
 #pragma unroll
-        for (int m = 16; m; m >>= 1) {
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-            low = min(low, __shfl_xor_sync(0xffffffffu, low, m));
-        }
-        live = __reduce_add_sync(0xffffffffu, live);
-        uint64_t edge = 1;      // keys above it are taken,
-        int32_t equal = 0;      // and this many of those equal to it
-        if (live > topk) {
-            // the largest edge with at least topk keys at or above it
-            int bit = 63 - __clzll(top ^ low);                          // -1: all alike
-            edge = bit < 0 ? top : top & ~((uint64_t(2) << bit) - 1);   // the common prefix
-            int32_t count = live;
-            for (; bit >= 0 && count != topk; --bit) {
-                const uint64_t trial = edge | (uint64_t(1) << bit);
-                int32_t cnt = 0;
-                for (int32_t p = lane; p < most; p += 32) cnt += key[p] >= trial;
-                cnt = __reduce_add_sync(0xffffffffu, cnt);
-                if (cnt >= topk) {
-                    edge = trial;
-                    count = cnt;
+        for (int m = 16; m; m >>= 1) bound += __shfl_xor_sync(0xffffffffu, bound, m);
+        // (an absolute part for products that underflow)
+        bound = fmaf(bound * __uint_as_float(max_mean), (D + 4) * 1.01f / 16777216.f, 1e-42f);
+        uint32_t cut = 1; // pages at or above it are taken, if they are at most topk
+        {
+            const Keys<uint32_t, kHeld> k(key32, most);
+            if (k.count(1) > topk) {
+                int32_t at;
+                const float tau = key_score(k.edge(topk, at));
+                // (not finite: a product or sum overflowed; every candidate is scored again)
+                const float low = tau - 2.02f * bound;
+                bool fine = fabsf(low) < INFINITY && k.count(score_key(-INFINITY)) == k.count(1);
+                cut = fine ? score_key(low) : 1u;
+                if (k.count(cut) > topk) {
+                    // some stay in doubt: those above the band certainly in (the largest key), below
+                    // it out (0), in it by their float64 score. From the last pages down, since a
+                    // 64-bit key covers two of the 32-bit ones.
+                    const uint32_t above = fine ? score_key(tau + 2.02f * bound) : ~0u;
+                    for (int32_t p0 = (most - 1) / 32 * 32; p0 >= 0; p0 -= 32) {
+                        const int32_t p = p0 + lane;
+                        const uint32_t x = p < most ? key32[p] : 0;
+                        uint64_t y = x > above && fine ? ~uint64_t(0) : 0;
+                        uint32_t doubt = __ballot_sync(0xffffffffu, y == 0 && x != 0 && x >= cut);
+                        while (doubt) {
+                            const int at_lane = __ffs(doubt) - 1;
+                            doubt &= doubt - 1;
+                            const int32_t page = cache_page(c, b, p0 + at_lane);
+                            const float *mean = summaries + (int64_t(page) * c.kv_heads + h) * D;
+                            double s = 0.0;
+                            for (int d = lane; d < D; d += 32) s = fma(q_sum(r, d), double(__ldg(mean + d)), s);
+#pragma unroll
+                            for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                            if (lane == at_lane) y = score_key(s);
+                        }
+                        __syncwarp();
+                        if (p < most) key64[p] = y;
+                        __syncwarp();
+                    }
+                    const Keys<uint64_t, 0> e(key64, most);
+                    int32_t count = e.count(1), equal = topk;
+                    uint64_t edge = 1;
+                    if (count > topk) {
+                        edge = e.edge(topk, count);
+                        if (count != topk) equal = edge == ~uint64_t(0) ? topk : topk - e.count(edge + 1);
+                    }
+                    write_bits(key64, most, edge, equal, dst, words);
+                    return;
                 }
             }
-            int32_t above = 0;
-            for (int32_t p = lane; p < most; p += 32) above += key[p] > edge;
-            equal = topk - __reduce_add_sync(0xffffffffu, above);
-            if (count == topk) equal = topk; // every key at or above the edge
-        } else {
-            equal = topk;
         }
-        int32_t seen = 0;
-        for (int32_t w = 0; w < words; ++w) {
-            const int32_t p = w * 32 + lane;
-            const uint64_t x = p < most ? key[p] : 0;
-            const bool even = x == edge && x != 0;
-            const uint32_t ties = __ballot_sync(0xffffffffu, even);
-            const int32_t rank = seen + __popc(ties & ((1u << lane) - 1));
-            const bool take = x > edge || (even && rank < equal);
-            seen += __popc(ties);
-            const uint32_t word = __ballot_sync(0xffffffffu, take);
-            if (lane == 0) dst[w] = word;
-        }
+        write_bits(key32, most, cut, most, dst, words);
+    };
+    for (int32_t r = warp; r < kRows && t0 + r < n; r += kWarps) {
+        if (most <= 128) choose(r, std::integral_constant<int, 4>{});
+        else if (most <= 512) choose(r, std::integral_constant<int, 16>{});
+        else choose(r, std::integral_constant<int, 0>{});
     }
 }
 
@@ -566,12 +685,12 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
 {
     auto kern = cache_select_kernel<D, kRows>;
     const size_t smem = size_t(kRows) * c.max_pages * 8;
-    if (smem > 48 * 1024) {
+    if (smem > 2 * 1024) { // (beside up to 46 KB of static shared memory)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(q.rows / kRows + c.batch, c.kv_heads);
-    kern<<<grid, 256, smem, stream>>>(c, q, summaries, topk, page_mask);
+    const dim3 grid(kRows > 1 ? q.rows / kRows + c.batch : q.rows, c.kv_heads);
+    kern<<<grid, select_warps(kRows) * 32, smem, stream>>>(c, q, summaries, topk, page_mask);
     return cudaGetLastError();
 }
 

@@ -233,6 +233,34 @@ def test_select_with_positions_ties_and_nan():
         assert np.array_equal(got.cpu().numpy(), C.words(want)), topk
 
 
+@pytest.mark.parametrize("D,size,pages,rows", [(64, 16, 40, 1), (128, 16, 300, 9), (64, 16, 1100, 3)])
+def test_select_of_scores_that_float32_cannot_tell_apart(D, size, pages, rows):
+    """Means equal but for last places: the order is that of the exact scores, ties to the lower page."""
+    cache, ref, rng = build(pages, [pages * size + rows], 1, D, size)
+    q = queries(rng, rows, 2, D)
+    base = rng.normal(size=D)
+    mean = torch.from_numpy(np.tile(base, (ref.k.shape[0], 1, 1))).float()
+    for c in range(ref.k.shape[0]):
+        d = int(rng.integers(0, D))
+        mean[c, 0, d] = torch.nextafter(mean[c, 0, d], torch.tensor(float("inf") if c % 3 else float("-inf")))
+    mean[5] = mean[1]
+    for topk in (1, 7, pages // 2):
+        got = ba.cache_select(cache, q.cuda(), i32([0, rows]), i32([pages * size]), mean.cuda(), size, 1, topk)
+        want = C.select(ref, f64(q), [0, rows], [pages * size], f64(mean), size, 1, topk)
+        assert np.array_equal(got.cpu().numpy(), C.words(want)), topk
+
+
+def test_select_of_scores_past_float32():
+    """Products that overflow float32 but not float64, and ones that underflow it."""
+    cache, ref, rng = build(3, [700], 1, 64, 16)
+    for scale_q, scale_m in ((2.0 ** 100, 2.0 ** 60), (2.0 ** -90, 2.0 ** -60), (2.0 ** -126, 1.0)):
+        q = (queries(rng, 2, 1, 64).double() * scale_q).to(torch.bfloat16)
+        mean = (torch.from_numpy(rng.normal(size=(ref.k.shape[0], 1, 64))) * scale_m).float()
+        got = ba.cache_select(cache, q.cuda(), i32([0, 2]), i32([698]), mean.cuda(), 16, 1, 5)
+        want = C.select(ref, f64(q), [0, 2], [698], f64(mean), 16, 1, 5)
+        assert np.array_equal(got.cpu().numpy(), C.words(want)), scale_q
+
+
 def test_select_skips_pages_without_a_number():
     cache, ref, rng = build(8, [300], 1, 64, 16)
     cache.page_table[0, 4] = -1
