@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t h = blockIdx.y, split = blockIdx.z;
     FwdTile t;
-    if (!find_tile(p, kR, t)) return;
+    if (!find_tile(p, blockIdx.x, kR, t)) return;
     const int col = lane % kLanes, set = lane / kLanes;
     RowView rv[kR];
     float2 q[kR][8];
@@ -321,11 +321,11 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
         const int64_t per = batch > 0 ? (int64_t(rows) + batch - 1) / batch : 0;
         if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
     }
-    // enough blocks for several on each of the 148 SMs, of no fewer than 256 slots
+    // enough items for several on each of the 148 SMs, of no fewer than 256 (512) slots
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
-    const int64_t items = (work > batch ? work : batch) * kv_heads;
+    const int64_t items = (work > batch ? work : batch) * kv_heads, least = mma ? 512 : 256;
     int64_t n = (148 * (mma ? 6 : 10) + items - 1) / (items > 0 ? items : 1);
-    const int64_t most = (reach + 255) / 256;
+    const int64_t most = (reach + least - 1) / least;
     if (n > most) n = most;
     if (n < 1) n = 1;
     int64_t chunk = ((reach + n - 1) / n + 63) / 64 * 64;

@@ -15,8 +15,8 @@ struct FwdTile {
     int32_t end;            // slots at and past it are empty
 };
 
-// Tile number blockIdx.x of `tile_rows` rows; false: the number is unused. Warp-collective.
-__device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, FwdTile &t)
+// Tile `number` of `tile_rows` rows; false: the number is unused. Warp-collective.
+__device__ __forceinline__ bool find_tile(const CacheFwd &p, int64_t number, int32_t tile_rows, FwdTile &t)
 {
     const int lane = threadIdx.x & 31;
     const int32_t *offs = p.q.q_offsets;
@@ -24,7 +24,7 @@ __device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, 
     while (n > 1) {
         const int32_t step = (n + 31) / 32, at = lo + lane * step;
         const bool ok = lane * step < n &&
-                        int64_t(__ldg(offs + at)) * p.q.group / tile_rows + (tile_rows > 1 ? at : 0) <= int64_t(blockIdx.x);
+                        int64_t(__ldg(offs + at)) * p.q.group / tile_rows + (tile_rows > 1 ? at : 0) <= number;
         const int32_t cnt = __popc(__ballot_sync(0xffffffffu, ok));
         n = min(step, n - (cnt - 1) * step);
         lo += (cnt - 1) * step;
@@ -33,13 +33,13 @@ __device__ __forceinline__ bool find_tile(const CacheFwd &p, int32_t tile_rows, 
     t.q0 = __ldg(offs + lo);
     t.n = __ldg(offs + lo + 1) - t.q0;
     const int64_t first = int64_t(t.q0) * p.q.group / tile_rows + (tile_rows > 1 ? lo : 0);
-    const int64_t row0 = (int64_t(blockIdx.x) - first) * tile_rows, all = int64_t(t.n) * p.q.group;
+    const int64_t row0 = (number - first) * tile_rows, all = int64_t(t.n) * p.q.group;
     if (row0 >= all) return false;
     t.row0 = int32_t(row0);
     t.rows = int32_t(min(all - row0, int64_t(tile_rows)));
     const int64_t cap = int64_t(p.c.max_pages) << p.c.page_shift;
     const int64_t len = max(__ldg(p.q.lens + lo), 0);
-    if (len + t.n > cap && threadIdx.x == 0) cache_range_error(p.c);
+    if (len + t.n > cap && lane == 0) cache_range_error(p.c);
     t.len = int32_t(min(len, cap));
     t.end = int32_t(min(len + t.n, cap));
     return true;

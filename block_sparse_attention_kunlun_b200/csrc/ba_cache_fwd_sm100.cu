@@ -15,18 +15,12 @@
 //
 // Roles of a block (512 threads, two blocks an SM, so that one block's softmax and set-up
 // overlap the other's MMAs):
-//   warps 0-3   softmax: thread t owns TMEM lane t
+//   warps 0-3   softmax: thread t owns row t (TMEM lane t)
 //   warps 4-11  dequantisation of a 64-slot tile
 //   warp 14     bulk copies of the tiles' codes
 //   warp 15     MMA issue (on another scheduler than the first softmax warps; 12 and 13 only
 //               fill the warpgroup, whose registers go to the softmax)
 // TMEM columns: O at 0, S at 128 (P over its first 32), Q at 192.
-//
-// S, softmax, P V and the next S follow one another, so the softmax's latency counts. A tile
-// of up to 64 rows leaves half of the 128 lanes empty: Q is then put there again, and the
-// second copy's softmax takes the tile's upper 32 slots (four copies and 16 slots each for
-// up to 32 rows). Each copy has its own running maximum, sum and O, with P zero in the other
-// columns; they are joined like splits when the tile is stored.
 //
 // Columns are kept in the order that widening four codes at once gives, 0 2 1 3 within each
 // four: Q is put in the same order as it is loaded, O is put back as it is stored.
@@ -72,13 +66,12 @@ struct MmaShared {
     // per tile (mod 16, more than can be under way): how many slots of each 16 there are, a byte each
     uint32_t there[16];
     uint64_t s_full, p_full, o_final;
-    uint64_t epi_sync;       // barrier of the softmax warps
     uint32_t tmem;
     int abort;
     int32_t min_ws, max_pos; // over the tile's rows
     int32_t nlist;
     int32_t odd_values;      // some value is NaN or infinite
-    float2 ml[kMmaRows];     // each lane's running maximum and sum
+    int32_t holes;           // some page has no number
     uint32_t wanted[kMmaList / 32 + 1];
     int32_t list[kMmaList];  // first slots of the listed units
 };
@@ -155,14 +148,14 @@ __device__ __forceinline__ uint64_t visible_bits(const CacheFwd &p, const FwdTil
 // below bf16's normal range round to its subnormals), columns in the order 0 2 1 3 within
 // each four. A code's sign, exponent and mantissa moved to a bf16's places (sign to bit 15,
 // the other seven bits to bits 10 .. 4) are the value times 2^-120, subnormal codes included;
-// one multiplication by 2^(e + 120) makes up for that and applies the scale. Past 2^127 the
-// factor is split in two. Returns whether a code is NaN (which this arithmetic does not know).
+// one multiplication by 2^(e + 120) makes up for that and applies the scale. Returns whether
+// that holds: not for a NaN code, nor for scales past 2^7, whose factor is none of bf16's
+// (widen4_any then).
 __device__ __forceinline__ bool widen16(const uint4 &codes, uint32_t scale_code, uint32_t (&out)[8])
 {
     const uint32_t ws[4] = {codes.x, codes.y, codes.z, codes.w};
-    const uint32_t field = scale_code + 120;
-    const uint32_t f1 = (field < 254 ? field : 254u) * 0x00800080u;
-    const __nv_bfloat162 s1 = *reinterpret_cast<const __nv_bfloat162 *>(&f1);
+    const uint32_t f = scale_code * 0x00800080u + 0x3c003c00u;
+    const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162 *>(&f);
     uint32_t nan = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -172,35 +165,27 @@ __device__ __forceinline__ bool widen16(const uint4 &codes, uint32_t scale_code,
                                ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u)};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x[j]), s1);
+            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x[j]), s);
             out[2 * i + j] = *reinterpret_cast<const uint32_t *>(&v);
         }
     }
-    if (field > 254) {
-        const uint32_t f2 = (field - 254 + 127) * 0x00800080u;
-        const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162 *>(&f2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&out[i]), s2);
-            out[i] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-    }
-    return nan & 0x80808080u;
+    return !(nan & 0x80808080u) && scale_code <= 134;
 }
 
-// Four codes with their widened form (two words), mended for what is rare (out of line, so
-// that the registers of the common path stay registers): NaNs are put in; with clear, NaNs
-// and infinities become 0 and *odd says that there were any.
-__device__ __noinline__ uint2 mend4(uint32_t codes, uint2 out, bool clear, int32_t *odd)
+// Four codes of any kind in the same form. With clear, NaNs and infinities become 0 and *odd
+// says that there were any. (Out of line and rare; its arguments are values, so that the
+// registers of the common path stay registers.)
+__device__ __noinline__ uint2 widen4_any(uint32_t codes, uint32_t scale_code, bool clear, int32_t *odd)
 {
-    uint32_t o[2] = {out.x, out.y};
+    uint32_t o[2] = {0u, 0u};
     for (int i = 0; i < 4; ++i) { // code i is in word i % 2, half i / 2
-        const int sh = 16 * (i / 2);
-        if (((codes >> (8 * i)) & 0x7fu) == 0x7fu) o[i % 2] |= 0x7fffu << sh;
-        if (clear && ((o[i % 2] >> sh) & 0x7f80u) == 0x7f80u) {
-            o[i % 2] &= ~(0xffffu << sh);
+        const float f = e4m3x2_to_f32((codes >> (8 * i)) & 0xffu).x * mx_scale(scale_code);
+        uint32_t v = __bfloat16_as_ushort(__float2bfloat16(f));
+        if (clear && (v & 0x7f80u) == 0x7f80u) {
+            v = 0;
             *odd = 1;
         }
+        o[i % 2] |= v << (16 * (i / 2));
     }
     return make_uint2(o[0], o[1]);
 }
@@ -270,10 +255,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t h = blockIdx.y, split = blockIdx.z;
     FwdTile t;
-    if (!find_tile(p, kMmaRows, t)) return;
-    // copies of the rows among the 128 lanes, and the softmax warps that have any
-    const int copies = t.rows <= 32 ? 4 : (t.rows <= 64 ? 2 : 1), lanes = kMmaRows / copies;
-    const int active = copies > 1 ? 4 : (t.rows + 31) / 32;
+    if (!find_tile(p, blockIdx.x, kMmaRows, t)) return;
+    const int active = (t.rows + 31) / 32; // softmax warps with rows
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
@@ -285,12 +268,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
         mbar_init(&sb.s_full, 1);
         mbar_init(&sb.p_full, active);
         mbar_init(&sb.o_final, 1);
-        mbar_init(&sb.epi_sync, 128);
         sb.abort = 0;
         sb.min_ws = INT32_MAX;
         sb.max_pos = -1;
         sb.nlist = 0;
         sb.odd_values = 0;
+        sb.holes = 0;
         fence_mbar_init();
     }
     if (p.page_mask)
@@ -305,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     const uint32_t tmem = sb.tmem;
     volatile int *abort = &sb.abort;
 
-    const int32_t row = t.row0 + min(tid % lanes, t.rows - 1);
+    const int32_t row = t.row0 + min(tid, t.rows - 1);
     const RowView rv = row_view(p, t, row); // (warps past the rows: the last row's)
     const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
     if (warp < active) {
@@ -386,34 +369,51 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     if (warp < 4) {
         warpgroup_regs_inc<kRegsSoftmax>();
         // ------------------------------------------------------ softmax ---
+        if (warp < active) {
+        const bool valid = tid < t.rows;
         const uint32_t s_addr = tmem + lane_base + Lay::kColS, o_addr = tmem + lane_base + Lay::kColO;
+        const int32_t last = min(rv.pos, t.len - 1); // cached slots from rv.ws to here are seen
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
-        // one tile's W columns from column W * copy on
-        auto softmax_tile = [&](int32_t i, uint64_t bits, auto width) {
-            constexpr int W = decltype(width)::value;
-            const int c0 = W == kKeys ? 0 : tid / lanes * W;
-            uint32_t sr[W];
-            if constexpr (W == 16) {
-                tmem_ld16(s_addr + c0, sr);
+        for (int32_t i = 0; i < sl.ntiles; ++i) {
+            uint64_t bits = 0;
+            if (!sl.listed) {
+                const int32_t s0 = sl.from + i * kKeys;
+                bits = s0 >= rv.ws && s0 + kKeys - 1 <= last ? ~uint64_t(0)
+                                                              : visible_bits(p, t, rv, h, s0, kKeys, sl.end);
             } else {
-#pragma unroll
-                for (int c = 0; c < W; c += 32) tmem_ld32(s_addr + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(sr + c));
+                for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
+                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end)
+                            << (k << sl.shift);
             }
-            tmem_wait_ld();
-            reg_fence(sr);
-            bits >>= c0;
+            if (!mbar_wait(&sb.s_full, i & 1, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (*const_cast<volatile int32_t *>(&sb.holes)) { // slots whose page has no number are unseen
+                const uint32_t there = sb.there[i % 16];
+                for (int g = 0; g < 4; ++g)
+                    if (((there >> (8 * g)) & 0xffu) == 0) bits &= ~(uint64_t(0xffff) << (16 * g));
+            }
             const uint32_t vis[2] = {uint32_t(bits), uint32_t(bits >> 32)};
-            const uint32_t all = W == 16 ? 0xffffu : 0xffffffffu;
-            const bool full = (vis[0] & all) == all && (W < kKeys || vis[1] == all);
-            if (!__all_sync(0xffffffffu, full)) {
+            const bool full = __all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu);
+            uint32_t sr[2][32];
+            tmem_ld32(s_addr, sr[0]);
+            tmem_ld32(s_addr + 32, sr[1]);
+            tmem_wait_ld();
+            reg_fence(sr[0]);
+            reg_fence(sr[1]);
+            if (!full) {
 #pragma unroll
-                for (int c = 0; c < W; ++c) sr[c] = (vis[c / 32] & (1u << (c % 32))) ? sr[c] : 0xff800000u;
+                for (int c = 0; c < kKeys; ++c)
+                    sr[c / 32][c % 32] = (vis[c / 32] & (1u << (c % 32))) ? sr[c / 32][c % 32] : 0xff800000u;
             }
             float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < W; c += 2)
-                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            for (int c = 0; c < kKeys; c += 2)
+                mp[(c / 2) % 4] = fmax3(mp[(c / 2) % 4], __uint_as_float(sr[c / 32][c % 32]),
+                                        __uint_as_float(sr[c / 32][c % 32 + 1]));
             const float m_new = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
             // O and l move to the new maximum only when it grew by more than 2^8
             float alpha = 1.f;
@@ -425,28 +425,17 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(neg_m, neg_m);
             float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            uint32_t pk[W / 2];
+            uint32_t pk[32];
 #pragma unroll
-            for (int c = 0; c < W / 2; ++c) {
-                const float2 x =
-                    ffma2(make_float2(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), sc2, nm2);
+            for (int c = 0; c < 32; ++c) {
+                const float2 x = ffma2(make_float2(__uint_as_float(sr[c / 16][2 * (c % 16)]),
+                                                   __uint_as_float(sr[c / 16][2 * (c % 16) + 1])),
+                                       sc2, nm2);
                 const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
                 acc[c % 2] = fadd2(acc[c % 2], make_float2(p0, p1));
                 pk[c] = pack_bf16x2(p0, p1);
             }
-            // P, zero in the other copies' columns
-            if constexpr (W == kKeys) {
-                tmem_st32(s_addr, pk);
-            } else if constexpr (W == 32) {
-                const uint32_t zero[16] = {};
-                tmem_st16(s_addr + c0 / 2, pk);
-                tmem_st16(s_addr + 16 - c0 / 2, zero);
-            } else {
-                const uint32_t zero[8] = {};
-                tmem_st8(s_addr + c0 / 2, pk);
-#pragma unroll
-                for (int x = 1; x < 4; ++x) tmem_st8(s_addr + (c0 / 2 + 8 * x) % 32, zero);
-            }
+            tmem_st32(s_addr, pk);
             const float2 sum = fadd2(acc[0], acc[1]);
             l = fmaf(l, alpha, sum.x + sum.y);
             // O holds the earlier tiles' P V (complete: this S was issued after it)
@@ -463,51 +452,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 }
             }
             tmem_wait_st();
-        };
-        for (int32_t i = 0; warp < active && i < sl.ntiles; ++i) {
-            uint64_t bits = 0;
-            if (!sl.listed) {
-                bits = visible_bits(p, t, rv, h, sl.from + i * kKeys, kKeys, sl.end);
-            } else {
-                for (int32_t k = 0; k < kKeys >> sl.shift; ++k)
-                    bits |= visible_bits(p, t, rv, h, unit_slot(sl, sb, i, k), unit, sl.end) << (k << sl.shift);
-            }
-            // slots whose page has no number are unseen
-            if (!mbar_wait(&sb.full[i % S], (i / S) & 1, abort)) {
-                ok = false;
-                break;
-            }
-            const uint32_t there = sb.there[i % 16];
-            if (there != 0x10101010u)
-                for (int g = 0; g < 4; ++g)
-                    if (((there >> (8 * g)) & 0xffu) == 0) bits &= ~(uint64_t(0xffff) << (16 * g));
-            if (!mbar_wait(&sb.s_full, i & 1, abort)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (copies == 4) softmax_tile(i, bits, std::integral_constant<int, 16>{});
-            else if (copies == 2) softmax_tile(i, bits, std::integral_constant<int, 32>{});
-            else softmax_tile(i, bits, std::integral_constant<int, 64>{});
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.p_full);
         }
-        // ----------------------------------------------------- epilogue ---
-        // the lanes' O, each at the maximum over its row's copies, through shared memory (the
-        // tiles are no longer needed: the last P V is complete) to rows written by whole warps
-        uint32_t phase = 0;
-        sb.ml[tid] = make_float2(m_ref, l);
-        if (ok && warp < active && sl.ntiles > 0) ok = mbar_wait(&sb.o_final, 0, abort);
-        ok = group_sync(&sb.epi_sync, phase, abort) && ok;
-        constexpr int kStride = D + 4; // floats a row, so that lanes' rows start in different banks
-        static_assert(kMmaRows * kStride * 4 <= Lay::kBytes, "staged O fits");
-        float *const stage = reinterpret_cast<float *>(smem);
-        if (ok && warp < active) {
+        if (ok && sl.ntiles > 0) ok = mbar_wait(&sb.o_final, 0, abort);
+        if (ok) {
             tc_fence_after();
-            float top = m_ref;
-            for (int x = 1; x < copies; ++x) top = fmaxf(top, sb.ml[(tid + x * lanes) % kMmaRows].x);
-            const float f = l == 0.f ? 0.f : ex2_approx(m_ref - top);
             OddValues<D> odd;
             const bool any_odd = sl.ntiles > 0 && *reinterpret_cast<volatile int32_t *>(&sb.odd_values);
             if (any_odd) { // (copies: objects whose address is taken would live in memory throughout)
@@ -518,6 +469,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 find_odd_values<D>(p, t2, r2, h, s2, sb, o2);
                 odd = o2;
             }
+            const int64_t oh = out_row(p, t, h, row);
+            const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
+            const bool whole = p.nsplit == 1;
+            const int64_t at = whole ? oh : int64_t(split) * p.q.rows * heads + oh;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // a part without any visible slot is left out by its statistics
+            const bool store = valid && (whole || l != 0.f);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -525,9 +483,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                     tmem_ld32(o_addr + c * 32, o);
                     tmem_wait_ld();
                     reg_fence(o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0;
                 }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+                for (int k = 0; k < 32; ++k)
+                    o[k] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) { // 0 2 1 3 back to 0 1 2 3
                     const uint32_t x = o[k + 1];
@@ -544,78 +506,59 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                         if ((odd.nan[c] & b) || (a && n)) o[k] = 0x7fffffffu;
                     }
                 }
+                if (store && whole) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<uint4 *>(stage + tid * kStride + 32 * c + k) =
-                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    for (int k = 0; k < 16; ++k)
+                        pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + 32 * c);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        dst[u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+                } else if (store) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + at * D + 32 * c);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        dst[u] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+                }
+            }
+            if (valid) {
+                if (whole) {
+                    const int64_t token = int64_t(t.q0) + row / p.q.group;
+                    p.lse[(int64_t(h) * p.q.group + row % p.q.group) * p.q.rows + token] =
+                        (m_ref + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    p.part_ml[at] = make_float2(m_ref, l);
+                }
             }
         }
-        ok = group_sync(&sb.epi_sync, phase, abort) && ok;
-        if (ok) {
-            constexpr int C = D / 32; // columns of a lane
-            const int64_t heads = int64_t(p.c.kv_heads) * p.q.group;
-            for (int r = warp; r < t.rows; r += 4) {
-                float top = -INFINITY, sum = 0.f, acc[C];
-                for (int x = 0; x < copies; ++x) top = fmaxf(top, sb.ml[r + x * lanes].x);
-#pragma unroll
-                for (int k = 0; k < C; ++k) acc[k] = 0.f;
-                for (int x = 0; x < copies; ++x) {
-                    const float2 ml = sb.ml[r + x * lanes];
-                    sum += ml.y == 0.f ? 0.f : ml.y * ex2_approx(ml.x - top);
-                    const float *src = stage + (r + x * lanes) * kStride + lane * C;
-#pragma unroll
-                    for (int k = 0; k < C; ++k) acc[k] += src[k];
-                }
-                const int64_t oh = out_row(p, t, h, t.row0 + r);
-                if (p.nsplit == 1) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-                    for (int k = 0; k < C; k += 2)
-                        *reinterpret_cast<uint32_t *>(p.out + oh * D + lane * C + k) =
-                            pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-                    if (lane == 0) {
-                        const int64_t token = oh / heads, head = oh % heads;
-                        p.lse[head * p.q.rows + token] = (top + log2f(sum)) * 0.6931471805599453f;
-                    }
-                } else {
-                    const int64_t at = int64_t(split) * p.q.rows * heads + oh;
-                    if (sum != 0.f) { // (a part without any visible slot is left out by its statistics)
-#pragma unroll
-                        for (int k = 0; k < C; k += 2)
-                            *reinterpret_cast<float2 *>(p.part_o + at * D + lane * C + k) =
-                                make_float2(acc[k], acc[k + 1]);
-                    }
-                    if (lane == 0) p.part_ml[at] = make_float2(top, sum);
-                }
-            }
         }
     } else if (warp < 12) {
         warpgroup_regs_dec<kRegsDequant>();
         // ----------------------------------------------- dequantisation ---
         constexpr int kLanes = D / 16, kRows = 256 / kLanes, kU = kKeys / kRows;
-        const int x = tid - 128, col = x % kLanes, r0 = x / kLanes;
-        // the two 16-byte units of this lane's 16 columns in a 128-byte row of their 64-column
-        // chunk; lanes of the upper chunk store them in the other order, so that eight
-        // consecutive lanes meet eight different units (no bank conflict)
-        const int flip = (col / 4) & 1, ua = (col % 4) * 2 + flip, ub = (col % 4) * 2 + 1 - flip;
+        // a lane's sixteen columns and first row. Of D = 128's two 64-column chunks, whose rows
+        // lie on the same banks, eight consecutive lanes take half a row each in two rows, so
+        // that neither their reads nor their swizzled stores meet a bank twice
+        const int x = tid - 128;
+        const int col = D == 128 ? (x & 3) | ((((x >> 2) ^ (x >> 3)) & 1) << 2) : x & 3;
+        const int r0 = D == 128 ? 2 * (x >> 4) + ((x >> 2) & 1) : x >> 2;
+        // its two 16-byte units in a 128-byte row of their chunk
+        const int ua = (((col % 4) * 2) ^ (r0 & 7)) << 4, ub = ua ^ 16;
         uint8_t *const chunk = smem + (col / 4) * Lay::kChunkBytes + r0 * 128;
         auto store = [&](uint8_t *dst, const uint4 &w, uint32_t sc, bool values) {
             uint32_t o[8];
-            const bool nan = widen16(w, sc, o);
-            // (448 * 2^119 is finite; only larger scales' products can overflow)
-            if (nan || (values && sc > 246)) {
+            if (!widen16(w, sc, o)) {
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const uint2 z = mend4(ws[y], make_uint2(o[2 * y], o[2 * y + 1]), values, &sb.odd_values);
+                    const uint2 z = widen4_any(ws[y], sc, values, &sb.odd_values);
                     o[2 * y] = z.x;
                     o[2 * y + 1] = z.y;
                 }
             }
-            *reinterpret_cast<uint4 *>(dst + ((ua ^ (r0 & 7)) << 4)) =
-                flip ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4 *>(dst + ((ub ^ (r0 & 7)) << 4)) =
-                flip ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4 *>(dst + ua) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(dst + ub) = make_uint4(o[4], o[5], o[6], o[7]);
         };
         static_assert(kRows % 8 == 0, "a lane's rows swizzle alike");
         for (int32_t i = 0; i < sl.ntiles; ++i) {
@@ -632,9 +575,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 vw[u] = *reinterpret_cast<const uint4 *>(raw + Lay::kRawV + r * D + col * 16);
                 ks[u] = raw[Lay::kRawKs + r * (D / 32) + col / 2];
                 vs[u] = raw[Lay::kRawVs + r * (D / 32) + col / 2];
-                if ((r & 15) >= int((there >> (8 * (r >> 4))) & 0xffu)) { // no such slot: zeros
-                    kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
-                    ks[u] = vs[u] = 127;
+            }
+            if (there != 0x10101010u) { // zeros where there is no slot
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int r = r0 + kRows * u;
+                    if ((r & 15) >= int((there >> (8 * (r >> 4))) & 0xffu)) {
+                        kw[u] = vw[u] = make_uint4(0u, 0u, 0u, 0u);
+                        ks[u] = vs[u] = 127;
+                    }
                 }
             }
             __syncwarp();
@@ -675,7 +624,10 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             int32_t count = 0; // slots of the piece that there are
             const int32_t us = slot_of(i);
             if (uint32_t(id) < uint32_t(p.c.num_pages)) count = min(sl.end - us, slots);
-            else if (mine && us < sl.end) cache_range_error(p.c);
+            else if (mine && us < sl.end) {
+                cache_range_error(p.c);
+                sb.holes = 1;
+            }
             uint32_t there = 0;
             if (mine && array == 0)
                 for (int32_t g = 0; g < slots / 16; ++g)
