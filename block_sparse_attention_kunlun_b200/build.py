@@ -20,7 +20,8 @@ OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["ba_api.cu", "ba_aux.cu", "ba_simt.cu", "ba_fwd_sm100.cu", "ba_bwd_dq_sm100.cu",
            "ba_bwd_dkdv_sm100.cu", "ba_noalloc.cu", "ba_rope.cu", "ba_mx.cu", "ba_cache.cu",
-           "ba_cache_fwd.cu", "ba_cache_fwd_sm100.cu"]
+           "ba_cache_fwd.cu", "ba_cache_fwd_sm100.cu",
+           "ba_cache_fwd_warp.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -312,7 +312,7 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     CacheFwdPlan plan;
     const int64_t all = int64_t(rows) * group; // query rows of a key/value head
     const int64_t each = batch > 0 ? (all + batch - 1) / batch : 1;
-    plan.tile_rows = each <= 1 ? 1 : (each <= 2 ? 2 : (each <= 4 ? 4 : kMmaRows));
+    plan.tile_rows = each <= 1 ? 1 : (each <= 8 ? 8 : (each <= 16 ? 16 : kMmaRows));
     const bool mma = plan.tile_rows == kMmaRows;
     plan.tiles = plan.tile_rows > 1 ? all / plan.tile_rows + batch : all;
     // the most slots a tile may meet: the whole cache, or the window and the rows themselves
@@ -356,9 +356,12 @@ cudaError_t launch_d(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t s
     if (plan.tile_rows == kMmaRows) {
         const cudaError_t e = launch_cache_fwd_mma<D>(p, plan, stream);
         if (e != cudaSuccess) return e;
-    } else if (plan.tile_rows == 1) launch_simt<D, 1>(p, plan, stream);
-    else if (plan.tile_rows == 2) launch_simt<D, 2>(p, plan, stream);
-    else launch_simt<D, 4>(p, plan, stream);
+    } else if (plan.tile_rows > 1) {
+        const cudaError_t e = launch_cache_fwd_warp<D>(p, plan, stream);
+        if (e != cudaSuccess) return e;
+    } else {
+        launch_simt<D, 1>(p, plan, stream);
+    }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.nsplit == 1) return e;
     const int64_t rows = int64_t(p.q.rows) * p.c.kv_heads * p.q.group;

@@ -90,6 +90,10 @@ constexpr int kMmaRows = 128;
 template <int D>
 cudaError_t launch_cache_fwd_mma(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream);
 
+// The kernel for 2 to 16 rows: plan.tile_rows 8 or 16.
+template <int D>
+cudaError_t launch_cache_fwd_warp(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream);
+
 // Units (pages, or halves of 128-slot pages) whose numbers a block of the tensor-core kernel
 // can list: with selected pages a split covers no more slots than that.
 constexpr int kMmaList = 2048;
