@@ -15,8 +15,8 @@
 //   O^T [16 columns x 8 rows] += V^T P^T: a lane reads 16 consecutive codes of four slots and
 //       pairs them slot by slot; which of the output's rows stands for which column is free
 //       too. P^T comes from S^T by movmatrix.
-// Codes are widened to bf16, exactly (as in ba_cache_fwd_sm100.cu); P is rounded to bf16. The
-// next 16 slots' codes are on their way while these are used. Codes that the widening does not
+// Codes are widened to bf16, exactly (as in ba_cache_fwd_sm100.cu); P is rounded to bf16. Values
+// are on their way while S is formed, the next slots' keys while P V is. Codes that the widening does not
 // know (NaN, scales past 2^7) take part in the MMAs as zeros, and their slots' scores, and their
 // values, are put in in float32: everything else stays the same to the bit.
 #include "ba_cache_fwd.cuh"
@@ -66,43 +66,52 @@ __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7
 
 // 16 slots' codes and scale codes as one lane (g = lane / 4, t = lane % 4) holds them.
 template <int D>
-struct Codes {
-    static constexpr int kKeyWords = D / 16, kValueWords = D / 32;
-    uint32_t k[2][kKeyWords];   // slots g, g + 8: 16 codes from 16 t on (D = 128: and from 64 + 16 t on)
-    uint32_t v[4][kValueWords]; // slots 2 t, 2 t + 1, 2 t + 8, 2 t + 9: D / 8 codes from D / 8 g on
-    uint32_t ks[2];             // the slots' scale codes, a byte a block
-    uint32_t vs[4];             // those of the codes' block
+struct KeyCodes {
+    static constexpr int kWords = D / 16;
+    uint32_t w[2][kWords]; // slots g, g + 8: 16 codes from 16 t on (D = 128: and from 64 + 16 t on)
+    uint32_t scales[2];    // the slots' scale codes, a byte a block
+
+    __device__ __forceinline__ void load(const CacheFwd &p, int64_t row)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t r = row + g + 8 * i;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.c.k + r * D) + t;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                const uint4 v = __ldg(src + 4 * x);
+                w[i][4 * x] = v.x, w[i][4 * x + 1] = v.y, w[i][4 * x + 2] = v.z, w[i][4 * x + 3] = v.w;
+            }
+            if constexpr (D == 128) scales[i] = __ldg(reinterpret_cast<const uint32_t *>(p.c.k_scales) + r);
+            else scales[i] = __ldg(reinterpret_cast<const uint16_t *>(p.c.k_scales) + r);
+        }
+    }
 };
 
 template <int D>
-__device__ __forceinline__ void load_codes(const CacheFwd &p, int64_t row, Codes<D> &c)
-{
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+struct ValueCodes {
+    static constexpr int kWords = D / 32;
+    uint32_t w[4][kWords]; // slots 2 t, 2 t + 1, 2 t + 8, 2 t + 9: D / 8 codes from D / 8 g on
+    uint32_t scale[4];     // scale codes of the codes' block
+
+    __device__ __forceinline__ void load(const CacheFwd &p, int64_t row)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t r = row + g + 8 * i;
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.c.k + r * D) + t;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-            const uint4 w = __ldg(src + 4 * x);
-            c.k[i][4 * x] = w.x, c.k[i][4 * x + 1] = w.y, c.k[i][4 * x + 2] = w.z, c.k[i][4 * x + 3] = w.w;
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = row + 2 * t + (i & 1) + 8 * (i >> 1);
+            if constexpr (D == 128) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.c.v + r * D) + g);
+                w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+            } else {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.c.v + r * D) + g);
+                w[i][0] = v.x, w[i][1] = v.y;
+            }
+            scale[i] = __ldg(p.c.v_scales + r * (D / 32) + g / (256 / D));
         }
-        if constexpr (D == 128) c.ks[i] = __ldg(reinterpret_cast<const uint32_t *>(p.c.k_scales) + r);
-        else c.ks[i] = __ldg(reinterpret_cast<const uint16_t *>(p.c.k_scales) + r);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = row + 2 * t + (i & 1) + 8 * (i >> 1);
-        if constexpr (D == 128) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.c.v + r * D) + g);
-            c.v[i][0] = w.x, c.v[i][1] = w.y, c.v[i][2] = w.z, c.v[i][3] = w.w;
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.c.v + r * D) + g);
-            c.v[i][0] = w.x, c.v[i][1] = w.y;
-        }
-        c.vs[i] = __ldg(p.c.v_scales + r * (D / 32) + g / (256 / D));
-    }
-}
+};
 
 // One lane's share of a tile's softmax: rows 2 t and 2 t + 1 of each eight. o[n][j]: columns
 // d = D / 8 g + 2 j (first two values) and d + 1 (last two) of rows 8 n + 2 t and 8 n + 2 t + 1.
@@ -125,31 +134,25 @@ __device__ __noinline__ float score_any(const __nv_bfloat16 *q, const uint8_t *k
 } // namespace
 
 template <int D, int kN>
-__global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
+__global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
     cache_fwd_warp_kernel(const __grid_constant__ CacheFwd p)
 {
     constexpr int kTiles = kN / 8;
     __shared__ float sm_o[kWarpCount][kN][D + 4];
     __shared__ float2 sm_ml[kWarpCount][kN];
+    __shared__ RowView views[kN];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int32_t h = blockIdx.y, split = blockIdx.z;
     FwdTile t;
     if (!find_tile(p, blockIdx.x, kN, t)) return;
 
-    // the lane's rows in the softmax, and Q's fragments: row g of each eight, in the codes' order
-    RowView rv[kTiles][2];
+    // the rows' views, and Q's fragments: row g of each eight, in the codes' order
+    if (threadIdx.x < kN) views[threadIdx.x] = row_view(p, t, t.row0 + min(int(threadIdx.x), t.rows - 1));
+    __syncthreads();
     uint32_t q[kTiles][D / 16][2];
-    int32_t min_ws = INT32_MAX, max_ws = 0, min_pos = INT32_MAX, max_pos = -1;
+    int32_t min_ws, max_ws, min_pos, max_pos;
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            rv[n][r] = row_view(p, t, t.row0 + min(8 * n + 2 * t4 + r, t.rows - 1));
-            min_ws = min(min_ws, rv[n][r].ws);
-            max_ws = max(max_ws, rv[n][r].ws);
-            min_pos = min(min_pos, rv[n][r].pos);
-            max_pos = max(max_pos, rv[n][r].pos);
-        }
         const uint4 *src = reinterpret_cast<const uint4 *>(
             p.q.q + out_row(p, t, h, t.row0 + min(8 * n + g, t.rows - 1)) * D + 16 * t4);
 #pragma unroll
@@ -163,10 +166,13 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
                 q[n][4 * x + 2 * u + 1][1] = __byte_perm(w.z, w.w, 0x7632);
             }
     }
-    min_ws = __reduce_min_sync(0xffffffffu, min_ws);
-    max_ws = __reduce_max_sync(0xffffffffu, max_ws);
-    min_pos = __reduce_min_sync(0xffffffffu, min_pos);
-    max_pos = __reduce_max_sync(0xffffffffu, max_pos);
+    {
+        const RowView v = views[lane % kN];
+        min_ws = __reduce_min_sync(0xffffffffu, v.ws);
+        max_ws = __reduce_max_sync(0xffffffffu, v.ws);
+        min_pos = __reduce_min_sync(0xffffffffu, v.pos);
+        max_pos = __reduce_max_sync(0xffffffffu, v.pos);
+    }
 
     // this split's slots, in groups of 16
     const int32_t lo = (p.page_mask ? 0 : min_ws) / kGroup * kGroup;
@@ -218,71 +224,59 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
         return true;
     };
 
-    auto take = [&](Codes<D> &c, int32_t slot, int64_t row) {
+    KeyCodes<D> keys;
+    ValueCodes<D> values;
+    int32_t next_slot;
+    int64_t next_row;
+    bool more = next_group(next_slot, next_row);
+    if (more) keys.load(p, next_row);
+    while (more) {
+        const int32_t slot = next_slot;
+        const int64_t row = next_row;
+        values.load(p, row);
         const bool all = slot >= max_ws && slot + kGroup - 1 <= min(min_pos, t.len - 1);
-        // codes that need the other path
-        uint32_t odd = 0, high = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int x = 0; x < Codes<D>::kKeyWords; ++x) odd |= nan_bits(c.k[i][x]);
-            // (a scale code over 134: its byte plus 121 carries into bit 8 of a 16-bit field)
-            high |= ((c.ks[i] & 0x00ff00ffu) + 0x00790079u) | (((c.ks[i] >> 8) & 0x00ff00ffu) + 0x00790079u);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int x = 0; x < Codes<D>::kValueWords; ++x) odd |= nan_bits(c.v[i][x]);
-            high |= c.vs[i] + 0x79u;
-        }
+        // codes that the widening does not know. (A scale code over 134: its byte plus 121 carries
+        // into bit 8 of a 16-bit field.)
         uint32_t odd_keys = 0, odd_values = 0; // slots with such codes
-        if (__any_sync(0xffffffffu, (odd & 0x80808080u) | (high & 0x01000100u))) {
+        {
+            uint32_t odd[2] = {0, 0}, high[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                odd = 0;
 #pragma unroll
-                for (int x = 0; x < Codes<D>::kKeyWords; ++x) odd |= nan_bits(c.k[i][x]);
-                high = ((c.ks[i] & 0x00ff00ffu) + 0x00790079u) | (((c.ks[i] >> 8) & 0x00ff00ffu) + 0x00790079u);
-                if ((odd & 0x80808080u) | (high & 0x01000100u)) odd_keys |= 1u << (g + 8 * i);
+                for (int x = 0; x < KeyCodes<D>::kWords; ++x) odd[i] |= nan_bits(keys.w[i][x]);
+                high[i] = ((keys.scales[i] & 0x00ff00ffu) + 0x00790079u) | (((keys.scales[i] >> 8) & 0x00ff00ffu) + 0x00790079u);
             }
-            odd_keys = __reduce_or_sync(0xffffffffu, odd_keys);
+            if (__any_sync(0xffffffffu, ((odd[0] | odd[1]) & 0x80808080u) | ((high[0] | high[1]) & 0x01000100u))) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if ((odd_keys >> (g + 8 * i)) & 1u) {
-                    c.ks[i] = 0;
+                for (int i = 0; i < 2; ++i)
+                    if ((odd[i] & 0x80808080u) | (high[i] & 0x01000100u)) odd_keys |= 1u << (g + 8 * i);
+                odd_keys = __reduce_or_sync(0xffffffffu, odd_keys);
 #pragma unroll
-                    for (int x = 0; x < Codes<D>::kKeyWords; ++x) c.k[i][x] = 0;
-                }
+                for (int i = 0; i < 2; ++i)
+                    if ((odd_keys >> (g + 8 * i)) & 1u) {
+                        keys.scales[i] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool big = c.vs[i] > 134;
-                odd = 0;
-#pragma unroll
-                for (int x = 0; x < Codes<D>::kValueWords; ++x) {
-                    const uint32_t nan = ((nan_bits(c.v[i][x]) & 0x80808080u) >> 7) * 0xffu;
-                    odd |= nan;
-                    c.v[i][x] = big ? 0u : c.v[i][x] & ~nan;
-                }
-                if (big) c.vs[i] = 0;
-                if (odd || big) odd_values |= 1u << (2 * t4 + (i & 1) + 8 * (i >> 1));
+                        for (int x = 0; x < KeyCodes<D>::kWords; ++x) keys.w[i][x] = 0;
+                    }
             }
-            odd_values = __reduce_or_sync(0xffffffffu, odd_values);
         }
         // S^T
         float sc[kTiles][4];
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
 #pragma unroll
-        for (int x = 0; x < Codes<D>::kKeyWords; ++x) {
+        for (int x = 0; x < KeyCodes<D>::kWords; ++x) {
             // block of the word's columns: (16 t + 64 (x / 4)) / 32
             const int shift = 8 * (t4 / 2 + 2 * (x / 4));
             uint32_t a[4];
-            widen4(c.k[0][x], bf16_factor((c.ks[0] >> shift) & 0xffu) * 0x00010001u, a[0], a[2]);
-            widen4(c.k[1][x], bf16_factor((c.ks[1] >> shift) & 0xffu) * 0x00010001u, a[1], a[3]);
+            widen4(keys.w[0][x], bf16_factor((keys.scales[0] >> shift) & 0xffu) * 0x00010001u, a[0], a[2]);
+            widen4(keys.w[1][x], bf16_factor((keys.scales[1] >> shift) & 0xffu) * 0x00010001u, a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) mma_16x8x16(sc[n], a, q[n][x][0], q[n][x][1]);
         }
         // softmax: values 0, 1 are slot g's for rows 2 t, 2 t + 1, values 2, 3 slot g + 8's
+        more = next_group(next_slot, next_row);
+        if (more) keys.load(p, next_row);
         if (odd_keys) {
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
@@ -310,7 +304,7 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
                 sc[n][e] *= p.scale_log2;
                 if (!all) {
                     const int32_t k = slot + g + 8 * (e >> 1);
-                    if (!(k < t.end && sees(p, t, rv[n][e & 1], h, k))) sc[n][e] = -INFINITY;
+                    if (!(k < t.end && sees(p, t, views[8 * n + 2 * t4 + (e & 1)], h, k))) sc[n][e] = -INFINITY;
                 }
                 grow |= sc[n][e] > s.m[n][e & 1] + 8.f;
             }
@@ -347,17 +341,42 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
             b[n][0] = transpose_8x8(pack_bf16x2(sc[n][0], sc[n][1]));
             b[n][1] = transpose_8x8(pack_bf16x2(sc[n][2], sc[n][3]));
         }
+        {
+            uint32_t odd = 0, high = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int x = 0; x < ValueCodes<D>::kWords; ++x) odd |= nan_bits(values.w[i][x]);
+                high |= values.scale[i] + 0x79u;
+            }
+            if (__any_sync(0xffffffffu, (odd & 0x80808080u) | (high & 0x100u))) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool big = values.scale[i] > 134;
+                    odd = 0;
+#pragma unroll
+                    for (int x = 0; x < ValueCodes<D>::kWords; ++x) {
+                        const uint32_t nan = ((nan_bits(values.w[i][x]) & 0x80808080u) >> 7) * 0xffu;
+                        odd |= nan;
+                        values.w[i][x] = big ? 0u : values.w[i][x] & ~nan;
+                    }
+                    if (big) values.scale[i] = 0;
+                    if (odd || big) odd_values |= 1u << (2 * t4 + (i & 1) + 8 * (i >> 1));
+                }
+                odd_values = __reduce_or_sync(0xffffffffu, odd_values);
+            }
+        }
         // O^T: slots 2 t, 2 t + 1 in the low and high halves of one register, 2 t + 8 and 2 t + 9 of
         // the other
-        const uint32_t f0 = bf16_factor(c.vs[0]) | bf16_factor(c.vs[1]) << 16;
-        const uint32_t f1 = bf16_factor(c.vs[2]) | bf16_factor(c.vs[3]) << 16;
+        const uint32_t f0 = bf16_factor(values.scale[0]) | bf16_factor(values.scale[1]) << 16;
+        const uint32_t f1 = bf16_factor(values.scale[2]) | bf16_factor(values.scale[3]) << 16;
 #pragma unroll
-        for (int x = 0; x < Codes<D>::kValueWords; ++x)
+        for (int x = 0; x < ValueCodes<D>::kWords; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) { // columns 4 x + 2 y, 4 x + 2 y + 1 of the lane's
                 uint32_t a[4];
-                widen4(__byte_perm(c.v[0][x], c.v[1][x], y ? 0x7632 : 0x5410), f0, a[0], a[1]);
-                widen4(__byte_perm(c.v[2][x], c.v[3][x], y ? 0x7632 : 0x5410), f1, a[2], a[3]);
+                widen4(__byte_perm(values.w[0][x], values.w[1][x], y ? 0x7632 : 0x5410), f0, a[0], a[1]);
+                widen4(__byte_perm(values.w[2][x], values.w[3][x], y ? 0x7632 : 0x5410), f1, a[2], a[3]);
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) mma_16x8x16(s.o[n][2 * x + y], a, b[n][0], b[n][1]);
             }
@@ -370,7 +389,7 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float w = __shfl_sync(0xffffffffu, k < 8 ? sc[n][r] : sc[n][2 + r], 4 * (k & 7) + t4);
-                    if (slot + k >= t.end || !sees(p, t, rv[n][r], h, slot + k)) continue;
+                    if (slot + k >= t.end || !sees(p, t, views[8 * n + 2 * t4 + r], h, slot + k)) continue;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -384,23 +403,6 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 3 : 2)
                         }
                 }
             __syncwarp();
-        }
-    };
-
-    // one set of codes is on its way while the other is used
-    {
-        Codes<D> next;
-        int32_t next_slot;
-        int64_t next_row;
-        bool more = next_group(next_slot, next_row);
-        if (more) load_codes<D>(p, next_row, next);
-        while (more) {
-            Codes<D> c = next;
-            const int32_t slot = next_slot;
-            const int64_t row = next_row;
-            more = next_group(next_slot, next_row);
-            if (more) load_codes<D>(p, next_row, next);
-            take(c, slot, row);
         }
     }
 
