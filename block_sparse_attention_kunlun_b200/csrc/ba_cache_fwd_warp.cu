@@ -71,20 +71,19 @@ struct KeyCodes {
     uint32_t w[2][kWords]; // slots g, g + 8: 16 codes from 16 t on (D = 128: and from 64 + 16 t on)
     uint32_t scales[2];    // the slots' scale codes, a byte a block
 
-    __device__ __forceinline__ void load(const CacheFwd &p, int64_t row)
+    // codes, scale codes: this lane's first ones of slot 0, `row` slots before these
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scale_codes, int64_t row)
     {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint8_t *const c = codes + row * D, *const s = scale_codes + row * (D / 32);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int64_t r = row + g + 8 * i;
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.c.k + r * D) + t;
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
-                const uint4 v = __ldg(src + 4 * x);
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(c + 8 * i * D + 64 * x));
                 w[i][4 * x] = v.x, w[i][4 * x + 1] = v.y, w[i][4 * x + 2] = v.z, w[i][4 * x + 3] = v.w;
             }
-            if constexpr (D == 128) scales[i] = __ldg(reinterpret_cast<const uint32_t *>(p.c.k_scales) + r);
-            else scales[i] = __ldg(reinterpret_cast<const uint16_t *>(p.c.k_scales) + r);
+            if constexpr (D == 128) scales[i] = __ldg(reinterpret_cast<const uint32_t *>(s + 8 * i * (D / 32)));
+            else scales[i] = __ldg(reinterpret_cast<const uint16_t *>(s + 8 * i * (D / 32)));
         }
     }
 };
@@ -95,20 +94,20 @@ struct ValueCodes {
     uint32_t w[4][kWords]; // slots 2 t, 2 t + 1, 2 t + 8, 2 t + 9: D / 8 codes from D / 8 g on
     uint32_t scale[4];     // scale codes of the codes' block
 
-    __device__ __forceinline__ void load(const CacheFwd &p, int64_t row)
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scale_codes, int64_t row)
     {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        const uint8_t *const c = codes + row * D, *const s = scale_codes + row * (D / 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = row + 2 * t + (i & 1) + 8 * (i >> 1);
+            const int at = (i & 1) + 8 * (i >> 1);
             if constexpr (D == 128) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p.c.v + r * D) + g);
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(c + at * D));
                 w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
             } else {
-                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p.c.v + r * D) + g);
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(c + at * D));
                 w[i][0] = v.x, w[i][1] = v.y;
             }
-            scale[i] = __ldg(p.c.v_scales + r * (D / 32) + g / (256 / D));
+            scale[i] = __ldg(s + at * (D / 32));
         }
     }
 };
@@ -220,21 +219,26 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
         const int x = __ffs(todo) - 1;
         todo &= todo - 1;
         slot = (base + x * kWarpCount + warp) * kGroup;
-        row = cache_row(p.c, __shfl_sync(0xffffffffu, id, x), h, slot & ((1 << p.c.page_shift) - 1));
+        row = int64_t(__shfl_sync(0xffffffffu, id, x)) * (p.c.kv_heads << p.c.page_shift) +
+              ((h << p.c.page_shift) + (slot & ((1 << p.c.page_shift) - 1)));
         return true;
     };
 
+    const uint8_t *const k_codes = p.c.k + g * D + 16 * t4, *const k_scales = p.c.k_scales + g * (D / 32);
+    const uint8_t *const v_codes = p.c.v + 2 * t4 * D + D / 8 * g;
+    const uint8_t *const v_scales = p.c.v_scales + 2 * t4 * (D / 32) + g / (256 / D);
+    const int32_t inside = min(min_pos, t.len - 1) - (kGroup - 1); // last slot whose 16 all rows see
     KeyCodes<D> keys;
     ValueCodes<D> values;
     int32_t next_slot;
     int64_t next_row;
     bool more = next_group(next_slot, next_row);
-    if (more) keys.load(p, next_row);
+    if (more) keys.load(k_codes, k_scales, next_row);
     while (more) {
         const int32_t slot = next_slot;
         const int64_t row = next_row;
-        values.load(p, row);
-        const bool all = slot >= max_ws && slot + kGroup - 1 <= min(min_pos, t.len - 1);
+        values.load(v_codes, v_scales, row);
+        const bool all = slot >= max_ws && slot <= inside;
         // codes that the widening does not know. (A scale code over 134: its byte plus 121 carries
         // into bit 8 of a 16-bit field.)
         uint32_t odd_keys = 0, odd_values = 0; // slots with such codes
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
         }
         // softmax: values 0, 1 are slot g's for rows 2 t, 2 t + 1, values 2, 3 slot g + 8's
         more = next_group(next_slot, next_row);
-        if (more) keys.load(p, next_row);
+        if (more) keys.load(k_codes, k_scales, next_row);
         if (odd_keys) {
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
