@@ -321,11 +321,14 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
         const int64_t per = batch > 0 ? (int64_t(rows) + batch - 1) / batch : 0;
         if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
     }
-    // enough items for several on each of the 148 SMs, of no fewer than 256 (512) slots
+    // Splits: as many as make kWaves full rounds of the blocks that 148 SMs hold at once (a part
+    // of a round more would leave most SMs waiting for it), none of fewer than 256 slots.
+    constexpr int64_t kWaves = 2;
+    const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? 7 : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
-    const int64_t items = (work > batch ? work : batch) * kv_heads, least = mma ? 512 : 256;
-    int64_t n = (148 * (mma ? 6 : 10) + items - 1) / (items > 0 ? items : 1);
-    const int64_t most = (reach + least - 1) / least;
+    const int64_t items = (work > batch ? work : batch) * kv_heads;
+    int64_t n = items > 0 ? kWaves * held / items : 1;
+    const int64_t most = (reach + 255) / 256;
     if (n > most) n = most;
     if (n < 1) n = 1;
     int64_t chunk = ((reach + n - 1) / n + 63) / 64 * 64;
