@@ -24,7 +24,6 @@ namespace ba {
 namespace {
 
 constexpr int kSimtWarps = 4;
-constexpr int kGroup = 16; // consecutive aligned slots, always of one page
 
 } // namespace
 
@@ -321,13 +320,16 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
         const int64_t per = batch > 0 ? (int64_t(rows) + batch - 1) / batch : 0;
         if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
     }
-    // Splits: as many as make kWaves full rounds of the blocks that 148 SMs hold at once (a part
-    // of a round more would leave most SMs waiting for it), none of fewer than 256 slots.
-    constexpr int64_t kWaves = 2;
+    // Splits: as many as fill the blocks that 148 SMs hold at once (some more would leave most SMs
+    // waiting for the rest), or three times that (twice on the tensor cores, whose blocks take
+    // longer to set up) where a split still has 1024 slots, none of fewer than 256. (Three rounds,
+    // two, one: one event over 16 long histories under four heads 237, 241, 271 us; 16 candidate
+    // sets with selected pages 129, 116, 117 us; 8 trees over windows, one round 34, two 43 us.)
     const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? 7 : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
     const int64_t items = (work > batch ? work : batch) * kv_heads;
-    int64_t n = items > 0 ? kWaves * held / items : 1;
+    int64_t n = items > 0 ? (mma ? 2 : 3) * held / items : 1;
+    if (n > 1 && reach / n < 1024) n = held / items;
     const int64_t most = (reach + 255) / 256;
     if (n > most) n = most;
     if (n < 1) n = 1;

@@ -85,6 +85,9 @@ __device__ __forceinline__ int64_t out_row(const CacheFwd &p, const FwdTile &t, 
     return token * p.c.kv_heads * p.q.group + h * p.q.group + row % p.q.group;
 }
 
+// The kernels for few rows take 16 consecutive aligned slots, always of one page, at a time.
+constexpr int kGroup = 16;
+
 // The tensor-core kernel: plan.tile_rows == kMmaRows.
 constexpr int kMmaRows = 128;
 template <int D>

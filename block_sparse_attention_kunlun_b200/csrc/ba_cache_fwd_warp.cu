@@ -28,7 +28,6 @@ namespace ba {
 namespace {
 
 constexpr int kWarpCount = 4;
-constexpr int kGroup = 16; // consecutive aligned slots, always of one page
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
