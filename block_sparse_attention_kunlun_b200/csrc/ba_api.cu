@@ -952,7 +952,7 @@ ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, cons
     if ((st = need_b200(num_sms)) != BA_OK) return st;
     const CacheQuery cq{static_cast<const __nv_bfloat16 *>(q), q_offsets, lens, positions, P.total_tokens,
                         P.heads / c.kv_heads, block, window};
-    BA_TRY(launch_cache_select(c, cq, summaries, topk, page_mask, num_sms, reinterpret_cast<cudaStream_t>(stream_)));
+    BA_TRY(launch_cache_select(c, cq, summaries, topk, page_mask, reinterpret_cast<cudaStream_t>(stream_)));
     return BA_OK;
 }
 

@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kRowThreads)
     constexpr int L = D / 8, kStep = kRowThreads / L, kBatch = 4;
     __shared__ int64_t target[kRowsPerBlock];
     const int32_t row0 = blockIdx.x * rows_per_block;
-    const int32_t n = min(rows_per_block, total_rows - row0);
+    // (rows behind the last sequence are nobody's)
+    const int32_t n = min(rows_per_block, min(total_rows, __ldg(row_offsets + c.batch)) - row0);
+    if (n <= 0) return;
     find_rows(c, row_offsets, starts, row0, n, target);
     const bool values = blockIdx.y != 0;
     const int d8 = threadIdx.x % L;
@@ -144,11 +146,14 @@ __global__ void __launch_bounds__(kRowThreads)
     constexpr int L = D / 16, kStep = kRowThreads / L, kBatch = 2;
     __shared__ int64_t target[kRowsPerBlock];
     const int32_t row0 = blockIdx.x * rows_per_block;
-    const int32_t n = min(rows_per_block, total_rows - row0);
+    // (rows behind the last sequence are nobody's)
+    const int32_t n = min(rows_per_block, min(total_rows, __ldg(row_offsets + c.batch)) - row0);
+    if (n <= 0) return;
     find_rows(c, row_offsets, starts, row0, n, target);
     const bool values = blockIdx.y != 0;
     const int d16 = threadIdx.x % L;
     T *dst = (values ? v : k) + int64_t(row0) * c.kv_heads * D + d16 * 16;
+    const bool wide = reinterpret_cast<uintptr_t>(dst) % 32 == 0; // (16-byte aligned tensors may be neither)
     const uint8_t *elems = values ? c.v : c.k, *scales = values ? c.v_scales : c.k_scales;
     const uint32_t heads = c.kv_heads, all = n * heads;
     for (uint32_t x0 = threadIdx.x / L; x0 < all; x0 += kBatch * kStep) {
@@ -187,10 +192,16 @@ __global__ void __launch_bounds__(kRowThreads)
                     o[2 * j + 1] = __float_as_uint(f.y);
                 }
             }
-            uint4 *out = reinterpret_cast<uint4 *>(dst + int64_t(x) * D);
+            T *const out = dst + int64_t(x) * D;
+            if (wide) { // whole sectors a store
 #pragma unroll
-            for (int j = 0; j < int(sizeof(T)); ++j)
-                __stcs(out + j, make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+                for (int j = 0; j < int(sizeof(T)) / 2; ++j) st_global_32b(out + j * (32 / sizeof(T)), o + 8 * j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < int(sizeof(T)); ++j)
+                    __stcs(reinterpret_cast<uint4 *>(out) + j,
+                           make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+            }
         }
     }
 }
@@ -512,8 +523,9 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
     const int32_t q0 = __ldg(q.q_offsets + b), n = __ldg(q.q_offsets + b + 1) - q0;
     const int32_t t0 = tile * kRows;
     if (t0 >= n) return;
-    const int32_t len = max(__ldg(q.lens + b), 0);
-    const int32_t full = min(len >> c.page_shift, c.max_pages); // pages below are full
+    const int32_t given = max(__ldg(q.lens + b), 0), len = min(given, c.max_pages << c.page_shift);
+    if (given > len && threadIdx.x == 0) cache_range_error(c);
+    const int32_t full = len >> c.page_shift; // pages below are full
     if (threadIdx.x < kRows) {
         // candidates of the row: pages that start before its window and are full
         int32_t cand = 0;
@@ -685,7 +697,8 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
 {
     auto kern = cache_select_kernel<D, kRows>;
     const size_t smem = size_t(kRows) * c.max_pages * 8;
-    if (smem > 2 * 1024) { // (beside up to 46 KB of static shared memory)
+    constexpr size_t kStatic = (select_warps(kRows) * 32 * kMeanStride + kRows * (D + 1)) * 4 + 64; // at most
+    if (kStatic + smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
@@ -697,7 +710,7 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
 } // namespace
 
 cudaError_t launch_cache_select(const CacheView &c, const CacheQuery &q, const float *summaries, int32_t topk,
-                                uint32_t *page_mask, int, cudaStream_t stream)
+                                uint32_t *page_mask, cudaStream_t stream)
 {
     // eight rows a block read each mean once; single events, and rows whose eight key arrays
     // would not fit in shared memory, go one row a block

@@ -108,7 +108,7 @@ __device__ __forceinline__ int32_t rule_start(const CacheQuery &q, int32_t pos)
 constexpr int32_t kSelectMaxPages = 16384;
 
 cudaError_t launch_cache_select(const CacheView &c, const CacheQuery &q, const float *summaries, int32_t topk,
-                                uint32_t *page_mask, int num_sms, cudaStream_t stream);
+                                uint32_t *page_mask, cudaStream_t stream);
 
 struct CacheFwd {
     CacheView c;

@@ -23,74 +23,57 @@ namespace ba {
 
 namespace {
 
-constexpr int kSimtWarps = 4;
+constexpr int kSimtWarps = 4; // 128 threads: one a column at the end
 
 } // namespace
 
-// A few query rows (kR) of one key/value head, on the CUDA cores: with one to four rows a
-// key, the bytes of the cache are the bound and a tensor-core tile would be all but empty.
+// One query row of one key/value head, on the CUDA cores: with one row a key, the bytes of the
+// cache are the bound and even a warp-wide matrix instruction would be all but empty.
 // A warp reads 16 slots of keys and of values, each a contiguous piece of its page, 16 bytes
 // (16 codes) a lane: D / 16 lanes hold a slot. They are widened to float32 in registers, a
 // score is a 16-term dot product in each lane and three (two) shuffles, and the value's lane
 // adds its 16 columns into its own running sum: each set of D / 16 lanes keeps the running
 // maximum and sum of the slots it has met, so the softmax needs no exchange inside the loop.
-// The sets and the warps are joined once at the end.
-template <int D, int kR>
+// The sets and the warps are joined once at the end. SIMT_FIGURES
+template <int D>
 __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const CacheFwd p)
 {
     constexpr int kLanes = D / 16;      // lanes of a slot
     constexpr int kSets = 32 / kLanes;  // slots of a load
     constexpr int kU = kGroup / kSets;  // loads of a group
-    __shared__ float sm_o[kSimtWarps][kR][D];
-    __shared__ float2 sm_ml[kSimtWarps][kR];
+    __shared__ float sm_o[kSimtWarps][D];
+    __shared__ float2 sm_ml[kSimtWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t h = blockIdx.y, split = blockIdx.z;
     FwdTile t;
-    if (!find_tile(p, blockIdx.x, kR, t)) return;
+    if (!find_tile(p, blockIdx.x, 1, t)) return;
     const int col = lane % kLanes, set = lane / kLanes;
-    RowView rv[kR];
-    float2 q[kR][8];
-    int32_t min_ws = INT32_MAX, max_ws = 0, min_pos = INT32_MAX, max_pos = -1;
+    const RowView rv = row_view(p, t, t.row0);
+    const int64_t oh = out_row(p, t, h, t.row0); // the row of q and out
+    float2 q[8];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        rv[r] = row_view(p, t, t.row0 + min(r, t.rows - 1));
-        min_ws = min(min_ws, rv[r].ws);
-        max_ws = max(max_ws, rv[r].ws);
-        min_pos = min(min_pos, rv[r].pos);
-        max_pos = max(max_pos, rv[r].pos);
-        const int32_t row = t.row0 + min(r, t.rows - 1);
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            p.q.q + ((int64_t(t.q0) + rv[r].tok) * p.c.kv_heads * p.q.group + h * p.q.group + row % p.q.group) * D +
-            col * 16);
+    for (int i = 0; i < 2; ++i) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.q.q + oh * D + col * 16) + i);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 w = __ldg(src + i);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                q[r][4 * i + x] = make_float2(__uint_as_float(ws[x] << 16) * p.scale_log2,
-                                              __uint_as_float(ws[x] & 0xffff0000u) * p.scale_log2);
-        }
+        for (int x = 0; x < 4; ++x)
+            q[4 * i + x] = make_float2(__uint_as_float(ws[x] << 16) * p.scale_log2,
+                                       __uint_as_float(ws[x] & 0xffff0000u) * p.scale_log2);
     }
     // this split's slots, in groups of 16
-    const int32_t lo = (p.page_mask ? 0 : min_ws) / kGroup * kGroup;
+    const int32_t lo = (p.page_mask ? 0 : rv.ws) / kGroup * kGroup;
     int64_t from = lo + int64_t(split) * p.chunk, to = split + 1 == p.nsplit ? t.end : from + p.chunk;
     if (to > t.end) to = t.end;
     // `from` is a multiple of 16; a split that starts past the end has nothing
     const int32_t g1 = int32_t((to + kGroup - 1) / kGroup), g0 = from < t.end ? int32_t(from / kGroup) : g1;
 
-    float m[kR], l[kR];
-    float2 o[kR][8];
+    float m = -INFINITY, l = 0.f;
+    float2 o[8];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[r][i] = make_float2(0.f, 0.f);
-    }
+    for (int i = 0; i < 8; ++i) o[i] = make_float2(0.f, 0.f);
 
-    // 16 slots at `slot` on page `id`; vis[r]: the slots that row r sees (kAll: every row all 16)
-    auto take = [&](int32_t slot, int32_t id, auto all_t, const uint32_t *vis) {
+    // 16 slots at `slot` on page `id`; vis: the slots that the row sees (kAll: all 16)
+    auto take = [&](int32_t slot, int32_t id, auto all_t, uint32_t vis) {
         constexpr bool kAll = decltype(all_t)::value;
         const int64_t row = cache_row(p.c, id, h, slot & ((1 << p.c.page_shift) - 1));
         const uint4 *ks = reinterpret_cast<const uint4 *>(p.c.k + row * D) + lane;
@@ -108,85 +91,62 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
             vw[u] = __ldg(vs + u * 32);
             vc[u] = __ldg(p.c.v_scales + srow + u * kSets * (D / 32));
         }
-        float s[kR][kU];
+        float s[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const uint32_t ws[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
-            float2 acc[kR];
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int r = 0; r < kR; ++r) acc[r] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
-#pragma unroll
-                for (int r = 0; r < kR; ++r) acc[r] = ffma2(q[r][i], f, acc[r]);
-            }
-            const float sc = mx_scale(kc[u]);
-#pragma unroll
-            for (int r = 0; r < kR; ++r) s[r][u] = (acc[r].x + acc[r].y) * sc;
+            for (int i = 0; i < 8; ++i)
+                acc = ffma2(q[i], e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), acc);
+            s[u] = (acc.x + acc.y) * mx_scale(kc[u]);
         }
+        float mx = m;
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
+        for (int u = 0; u < kU; ++u) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
+            for (int x = 1; x < kLanes; x <<= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
+            if (!kAll) s[u] = (vis >> (u * kSets + set)) & 1u ? s[u] : -INFINITY;
+            mx = fmaxf(mx, s[u]);
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float alpha = ex2_approx(m - ref);
+        m = mx;
+        float sum = 0.f;
 #pragma unroll
-                for (int x = 1; x < kLanes; x <<= 1) s[r][u] += __shfl_xor_sync(0xffffffffu, s[r][u], x);
-                if (!kAll) s[r][u] = (vis[r] >> (u * kSets + set)) & 1u ? s[r][u] : -INFINITY;
-            }
+        for (int u = 0; u < kU; ++u) {
+            s[u] = ex2_approx(s[u] - ref);
+            sum += s[u];
+        }
+        l = fmaf(l, alpha, sum);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
-            float mx = m[r];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) mx = fmaxf(mx, s[r][u]);
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            const float alpha = ex2_approx(m[r] - ref);
-            m[r] = mx;
-            float sum = 0.f;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                s[r][u] = ex2_approx(s[r][u] - ref);
-                sum += s[r][u];
-            }
-            l[r] = fmaf(l[r], alpha, sum);
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[r][i] = fmul2(o[r][i], a2);
-            }
+            for (int i = 0; i < 8; ++i) o[i] = fmul2(o[i], a2);
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
+            // a slot that the row does not see may hold anything (0 * NaN is NaN)
+            if (!kAll && !((vis >> (u * kSets + set)) & 1u)) continue;
             const uint32_t ws[4] = {vw[u].x, vw[u].y, vw[u].z, vw[u].w};
-            const float sc = mx_scale(vc[u]);
-            float2 pr[kR];
+            const float pr = s[u] * mx_scale(vc[u]);
+            const float2 pr2 = make_float2(pr, pr);
 #pragma unroll
-            for (int r = 0; r < kR; ++r) pr[r] = make_float2(s[r][u] * sc, s[r][u] * sc);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu);
-#pragma unroll
-                for (int r = 0; r < kR; ++r) {
-                    // a slot that the row does not see may hold anything (0 * NaN is NaN)
-                    if (kAll) o[r][i] = ffma2(pr[r], f, o[r][i]);
-                    else if ((vis[r] >> (u * kSets + set)) & 1u) o[r][i] = ffma2(pr[r], f, o[r][i]);
-                }
-            }
+            for (int i = 0; i < 8; ++i)
+                o[i] = ffma2(pr2, e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), o[i]);
         }
     };
 
     for (int32_t base = g0; base < g1; base += kSimtWarps * 32) {
-        // 32 groups of this warp: which of them any row may see, and their pages
+        // 32 groups of this warp: which of them the row may see, and their pages
         const int32_t g = base + lane * kSimtWarps + warp, slot = g * kGroup;
-        bool want = g < g1 && (slot + kGroup > min_ws || slot + kGroup > t.len);
+        bool want = g < g1 && (slot + kGroup > rv.ws || slot + kGroup > t.len);
         if (g < g1 && !want && p.page_mask) {
             const int32_t page = slot >> p.c.page_shift;
-#pragma unroll
-            for (int r = 0; r < kR; ++r)
-                want |= (__ldg(p.page_mask +
-                               ((int64_t(t.q0) + rv[r].tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
-                         (page & 31)) & 1u;
+            want = (__ldg(p.page_mask + ((int64_t(t.q0) + rv.tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
+                    (page & 31)) & 1u;
         }
-        want = want && (slot <= max_pos || slot + kGroup > t.len);
+        want = want && (slot <= rv.pos || slot + kGroup > t.len);
         int32_t id = -1;
         if (want) {
             id = cache_page(p.c, t.b, slot >> p.c.page_shift);
@@ -198,74 +158,59 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
             todo &= todo - 1;
             const int32_t s0 = (base + x * kSimtWarps + warp) * kGroup;
             const int32_t page = __shfl_sync(0xffffffffu, id, x);
-            if (s0 >= max_ws && s0 + kGroup - 1 <= min(min_pos, t.len - 1)) {
-                take(s0, page, std::true_type{}, nullptr);
-            } else {
-                uint32_t vis[kR];
-#pragma unroll
-                for (int r = 0; r < kR; ++r)
-                    vis[r] = __ballot_sync(0xffffffffu, lane < kGroup && s0 + lane < t.end &&
-                                                            sees(p, t, rv[r], h, s0 + lane));
-                take(s0, page, std::false_type{}, vis);
-            }
+            if (s0 >= rv.ws && s0 + kGroup - 1 <= min(rv.pos, t.len - 1))
+                take(s0, page, std::true_type{}, 0u);
+            else
+                take(s0, page, std::false_type{},
+                     __ballot_sync(0xffffffffu, lane < kGroup && s0 + lane < t.end && sees(p, t, rv, h, s0 + lane)));
         }
     }
 
     // join the sets of lanes, then the warps
+    float mx = m;
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-        float mx = m[r];
+    for (int x = kLanes; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    const float a = ex2_approx(m - (mx == -INFINITY ? 0.f : mx));
+    l *= a;
 #pragma unroll
-        for (int x = kLanes; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float a = ex2_approx(m[r] - (mx == -INFINITY ? 0.f : mx));
-        l[r] *= a;
+    for (int x = kLanes; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
 #pragma unroll
-        for (int x = kLanes; x < 32; x <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+    for (int i = 0; i < 8; ++i) {
+        o[i].x *= a;
+        o[i].y *= a;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[r][i].x *= a;
-            o[r][i].y *= a;
-#pragma unroll
-            for (int x = kLanes; x < 32; x <<= 1) {
-                o[r][i].x += __shfl_xor_sync(0xffffffffu, o[r][i].x, x);
-                o[r][i].y += __shfl_xor_sync(0xffffffffu, o[r][i].y, x);
-            }
+        for (int x = kLanes; x < 32; x <<= 1) {
+            o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, x);
+            o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, x);
         }
-        if (set == 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<float2 *>(&sm_o[warp][r][col * 16 + 2 * i]) = o[r][i];
-        }
-        if (lane == 0) sm_ml[warp][r] = make_float2(mx, l[r]);
     }
+    if (set == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float2 *>(&sm_o[warp][col * 16 + 2 * i]) = o[i];
+    }
+    if (lane == 0) sm_ml[warp] = make_float2(mx, l);
     __syncthreads();
+    const int32_t d = threadIdx.x;
+    if (d >= D) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) top = fmaxf(top, sm_ml[w].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSimtWarps; ++w) {
+        const float x = ex2_approx(sm_ml[w].x - ref);
+        sum = fmaf(sm_ml[w].y, x, sum);
+        acc = fmaf(sm_o[w][d], x, acc);
+    }
     const int32_t heads = p.c.kv_heads * p.q.group;
-    for (int x = threadIdx.x; x < t.rows * D; x += kSimtWarps * 32) {
-        const int r = x / D, d = x % D;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kSimtWarps; ++w) mx = fmaxf(mx, sm_ml[w][r].x);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < kSimtWarps; ++w) {
-            const float a = ex2_approx(sm_ml[w][r].x - ref);
-            sum = fmaf(sm_ml[w][r].y, a, sum);
-            acc = fmaf(sm_o[w][r][d], a, acc);
-        }
-        const int32_t row = t.row0 + r;
-        const int64_t token = int64_t(t.q0) + row / p.q.group;
-        const int32_t head = h * p.q.group + row % p.q.group;
-        const int64_t oh = token * heads + head;
-        if (p.nsplit == 1) {
-            p.out[oh * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
-            if (d == 0)
-                p.lse[int64_t(head) * p.q.rows + token] = (mx + log2f(sum)) * 0.6931471805599453f;
-        } else {
-            const int64_t at = int64_t(split) * p.q.rows * heads + oh;
-            p.part_o[at * D + d] = acc;
-            if (d == 0) p.part_ml[at] = make_float2(mx, sum);
-        }
+    if (p.nsplit == 1) {
+        p.out[oh * D + d] = __float2bfloat16(sum == 0.f ? 0.f : acc / sum);
+        if (d == 0) p.lse[oh % heads * p.q.rows + oh / heads] = (top + log2f(sum)) * 0.6931471805599453f;
+    } else {
+        const int64_t at = int64_t(split) * p.q.rows * heads + oh;
+        p.part_o[at * D + d] = acc;
+        if (d == 0) p.part_ml[at] = make_float2(top, sum);
     }
 }
 
@@ -278,7 +223,7 @@ __global__ void __launch_bounds__(256) cache_combine_kernel(const CacheFwd p)
     const int lane = threadIdx.x & 31;
     const int32_t heads = p.c.kv_heads * p.q.group;
     const int64_t all = int64_t(p.q.rows) * heads, at = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (at >= all) return;
+    if (at >= all || at / heads >= __ldg(p.q.q_offsets + p.c.batch)) return; // (rows behind the last sequence)
     float mx = -INFINITY;
     for (int32_t s = 0; s < p.nsplit; ++s) mx = fmaxf(mx, p.part_ml[s * all + at].x);
     const float ref = mx == -INFINITY ? 0.f : mx;
@@ -348,13 +293,6 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
 
 namespace {
 
-template <int D, int kR>
-void launch_simt(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
-{
-    const dim3 grid(unsigned(plan.tiles), unsigned(p.c.kv_heads), unsigned(p.nsplit));
-    cache_fwd_simt_kernel<D, kR><<<grid, kSimtWarps * 32, 0, stream>>>(p);
-}
-
 template <int D>
 cudaError_t launch_d(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t stream)
 {
@@ -365,7 +303,8 @@ cudaError_t launch_d(const CacheFwd &p, const CacheFwdPlan &plan, cudaStream_t s
         const cudaError_t e = launch_cache_fwd_warp<D>(p, plan, stream);
         if (e != cudaSuccess) return e;
     } else {
-        launch_simt<D, 1>(p, plan, stream);
+        const dim3 grid(unsigned(plan.tiles), unsigned(p.c.kv_heads), unsigned(p.nsplit));
+        cache_fwd_simt_kernel<D><<<grid, kSimtWarps * 32, 0, stream>>>(p);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.nsplit == 1) return e;

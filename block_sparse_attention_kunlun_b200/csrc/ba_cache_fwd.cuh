@@ -1,6 +1,6 @@
-// What the two attention kernels over the history cache (ba_cache_fwd.cu: a few query
-// rows, CUDA cores; ba_cache_fwd_sm100.cu: up to 128, tensor cores) share: a block's tile of
-// query rows and which slots a row sees.
+// What the three attention kernels over the history cache (ba_cache_fwd.cu: one query row,
+// CUDA cores; ba_cache_fwd_warp.cu: 8 or 16, warp-wide MMAs; ba_cache_fwd_sm100.cu: 128,
+// tcgen05) share: a block's tile of query rows and which slots a row sees.
 #pragma once
 
 #include "ba_cache.cuh"

@@ -37,6 +37,16 @@ namespace ba {
 
 namespace {
 
+// Copy of `bytes` consecutive bytes into shared memory, completing on `bar`; both addresses
+// and the size must be multiples of 16.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 constexpr int kKeys = 64; // slots of a tile
 constexpr int kThreads = 512;
 constexpr int kCopyWarp = 14, kMmaWarp = 15;
@@ -633,6 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 for (int32_t g = 0; g < slots / 16; ++g)
                     there |= uint32_t(max(0, min(16, count - 16 * g))) << (8 * (piece * (slots / 16) + g));
             there = __reduce_or_sync(0xffffffffu, there);
+            __syncwarp(); // (holes, before lane 0 arrives)
             const uint32_t bytes = count > 0 ? slots * row_bytes : 0;
             const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
             if (!mbar_wait(&sb.raw_empty[rs], ((i / Lay::kRawStages) & 1) ^ 1, abort)) break;

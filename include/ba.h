@@ -399,17 +399,18 @@ typedef struct {
  * head_dim] tensors, float32 or bf16) is quantised into slot starts[b] + t.
  * Scale and elements as ba_mx_quantize's. A NaN does not count for its
  * block's scale and becomes E4M3's NaN; an infinity sets the scale to 2^120
- * and becomes the largest code, 448 (which reads back as infinity). Rows whose slot is negative, past
- * max_pages or without a page are skipped, and the status word says so.
+ * and becomes the largest code, 448 (which reads back as infinity). Rows
+ * whose slot is negative, past max_pages or without a page are skipped, and
+ * the status word says so.
  *
  * ba_cache_read: the reverse: row t of sequence b of k and v receives slot
  * starts[b] + t as element * 2^e, rounded to the nearest bf16 (exact unless
  * subnormal) or exact in float32. A slot that does not exist gives zeros
  * and sets the status word.
  *
- * row_offsets: DEVICE int32 [batch + 1], row_offsets[0] = 0, non-decreasing,
- * row_offsets[batch] = total_rows (not checked on the device); starts: DEVICE
- * int32 [batch].
+ * row_offsets: DEVICE int32 [batch + 1], row_offsets[0] = 0, non-decreasing
+ * (not checked on the device); dense rows from row_offsets[batch] on are not
+ * read or written; starts: DEVICE int32 [batch].
  */
 ba_status ba_cache_write(const ba_cache *cache, ba_dtype dtype, const void *k, const void *v,
                          const int32_t *row_offsets, const int32_t *starts, int32_t total_rows, ba_stream_t stream);
@@ -433,8 +434,10 @@ ba_status ba_cache_summarize(const ba_cache *cache, const int32_t *starts, const
  * The problem describes the queries: q DEVICE bf16 [total_tokens, heads,
  * head_dim], heads a multiple of the cache's kv_heads (query head x uses
  * key/value head x / (heads / kv_heads)), batch and head_dim the cache's;
- * sequence b owns rows q_offsets[b] .. q_offsets[b+1]-1. lens: DEVICE int32
- * [batch], the cached slots of each sequence. positions: DEVICE int32
+ * sequence b owns rows q_offsets[b] .. q_offsets[b+1]-1 (q_offsets[0] = 0,
+ * non-decreasing, none above total_tokens: not checked on the device), and
+ * what belongs to rows from q_offsets[batch] on is left as it was. lens:
+ * DEVICE int32 [batch], the cached slots of each sequence. positions: DEVICE int32
  * [total_tokens], each query's position in its history, or NULL for
  * lens[b] + t (row t of sequence b).
  *
@@ -467,10 +470,11 @@ ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, cons
  *     (tree_mask NULL: j <= t).
  * tree_mask: DEVICE uint32 [total_tokens, tree_words], bit j % 32 of word
  * j / 32 for row j of the same sequence; rows past tree_words * 32 are not
- * seen. With page_mask, max_pages <= 16384 (else BA_ERR_UNSUPPORTED). A row without tree_mask and positions is what ba_fwd computes for the
- * event at that position, on the dequantised keys and values, and so is each
- * row of a tree for the history that ends in its path. out: DEVICE bf16 like
- * q; lse: DEVICE float32 [heads, total_tokens]. A row that sees nothing
+ * seen. With page_mask, max_pages <= 16384 (else BA_ERR_UNSUPPORTED). A row
+ * without tree_mask and positions is what ba_fwd computes for the event at
+ * that position, on the dequantised keys and values, and so is each row of a
+ * tree for the history that ends in its path. out: DEVICE bf16 like q; lse:
+ * DEVICE float32 [heads, total_tokens]. A row that sees nothing
  * gets out = 0 and lse = -infinity; what a row does not see, NaN and
  * infinity included, does not reach it. Queries at negative positions see
  * nothing.

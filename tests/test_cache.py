@@ -61,9 +61,10 @@ def attention_bound(ref, D):
     return tol_out, tol_lse
 
 
-def check_attention(got, ref, D):
+def check_attention(got, ref, D, more=0.0):
     out, lse = f64(got[0]), f64(got[1])
     tol_out, tol_lse = attention_bound(ref, D)
+    tol_out = tol_out + more
     assert np.array_equal(np.isneginf(lse), np.isneginf(ref[1]))
     seen = np.isfinite(ref[1])
     assert np.all(np.abs(lse - ref[1])[seen] <= tol_lse[seen]), np.max((np.abs(lse - ref[1]) - tol_lse)[seen])
@@ -508,6 +509,154 @@ def test_element_offsets_past_32_bits():
     assert ba.ba_device_status(cache.status) == ba.BA_OK
 
 
+# Sequences whose rows take several tiles of 8 or 16 rows, beside ones with a row or none.
+MIDDLE = [
+    # D, size, kv, group, lens, rows, block, window, kind, selected
+    (128, 64, 1, 4, [900, 333], [3, 4], 256, 2, "chain", 0),
+    (64, 16, 2, 3, [200, 50, 0], [5, 4, 3], 32, 1, "tree", 0),
+    (128, 16, 1, 1, [300, 40, 40, 40], [30, 1, 1, 1], 64, 1, "tree", 3),
+    (64, 128, 1, 2, [600, 100, 5], [20, 1, 1], 128, 1, "candidates", 2),
+    (64, 32, 1, 1, [400, 9, 9], [17, 1, 0], 64, 1, "ragged", 4),
+    (128, 32, 3, 1, [0], [12], 16, 3, "ragged", 0),
+    (128, 128, 1, 2, [513, 128], [1, 6], 1 << 20, 1, "chain", 0),
+    (128, 64, 2, 1, [64, 700], [33, 0], 96, 1, "past", 0),
+    (64, 16, 1, 2, [90, 17, 256], [4, 2, 9], 32, 2, "past", 3),
+    (128, 16, 1, 1, [90, 17, 256], [4, 2, 9], 32, 2, "past", 0),
+    (64, 64, 2, 1, [500, 1, 70], [1, 1, 1], 64, 1, "past", 2),
+]
+
+
+@pytest.mark.parametrize("D,size,kv,group,lens,n,block,window,kind,selected", MIDDLE)
+def test_attention_of_uneven_batches(D, size, kv, group, lens, n, block, window, kind, selected):
+    if kind != "past":
+        test_attention_matches_the_oracle(D, size, kv, group, lens, n, block, window, kind, selected, 2.0)
+        return
+    # positions in any order, before the history's end and before its start, without a tree
+    cache, ref, rng = build(D + size + len(n), [a + b for a, b in zip(lens, n)], kv, D, size)
+    rows, offs = sum(n), offsets(n)
+    q = queries(rng, rows, kv * group, D)
+    pos = [int(rng.integers(-2, lens[b] + n[b])) for b in range(len(n)) for _ in range(n[b])]
+    mask = None
+    if selected:
+        mask = C.words(rng.random((rows, kv, ref.table.shape[1])) < selected / ref.table.shape[1])
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32(offs), i32(lens), block, window, positions=i32(pos),
+                                 page_mask=None if mask is None else i32(mask))
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+    check_attention(got, C.attend(ref, f64(q), offs, lens, block, window, pos, None, mask), D)
+
+
+@pytest.mark.parametrize("rows,D", [(5, 128), (5, 64), (7, 128), (7, 64)])
+def test_long_cache_split_over_blocks_of_8_and_16_rows(rows, D):
+    test_long_cache_split_over_blocks(rows, D)
+
+
+ROWS = [1, 6, 12, 40]   # of one sequence: each of the attention's kernels
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+def test_values_and_keys_of_any_scale(rows, D):
+    """Scales over the whole range, past those the fast widening knows and below bf16's normal numbers."""
+    cache, ref, rng = build(rows + D, [90 + rows], 2, D, 32)
+    for t, low, high in ((cache.v_scales, 0, 200), (cache.k_scales, 90, 131)):
+        old = t.cpu()
+        some = torch.from_numpy(rng.random(tuple(old.shape)) < 0.3)
+        old[some] = torch.from_numpy(rng.integers(low, high, tuple(old.shape)).astype(np.uint8))[some]
+        t.copy_(old)
+    ref = C.Cache(*(t.cpu().numpy() for t in (cache.k, cache.v, cache.k_scales, cache.v_scales, cache.page_table)))
+    q = queries(rng, rows, 2, D)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32([0, rows]), i32([90]), 1 << 20, 1)
+    # Values reach 2^73 * 448 here while scores differ by hundreds, so what float32's range leaves out counts: a
+    # probability below 2^-126 of its reference becomes 0, and so does a warp's or a split's weight. A reference is
+    # at most 2^8 below the largest score, the final sum at least 1, so each of the three loses at most
+    # 2^8 2^-126 |v| of a slot: 3 2^-118 sum |v| in all.
+    seen = np.stack([ref.v[ref.slot(0, p)[0], :, ref.slot(0, p)[1]] for p in range(90 + rows)])
+    check_attention(got, C.attend(ref, f64(q), [0, rows], [90], 1 << 20, 1), D,
+                    more=3 * 2.0 ** -118 * np.abs(seen).sum(axis=0))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_sequences_that_share_pages(rows):
+    """Two sequences on the same pages of a common beginning, with pages of their own after it."""
+    cache, ref, rng = build(rows, [128 + rows, 96 + rows], 1, 128, 32)
+    cache.page_table[1, :3] = cache.page_table[0, :3]
+    ref.table[1, :3] = ref.table[0, :3]
+    n, lens = [rows, rows], [128, 96]
+    q = queries(rng, 2 * rows, 1, 128)
+    mean = torch.zeros((ref.k.shape[0], 1, 128), device="cuda")
+    ba.cache_summarize(cache, i32([0, 0]), i32(lens), mean)
+    want = C.summarize(ref, [0, 0], lens, np.zeros(mean.shape))
+    mag = np.maximum(np.abs(ref.k).mean(axis=2), 1e-30)
+    assert np.all(np.abs(f64(mean) - want) <= 32 * 2.0 ** -24 * mag)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32(offsets(n)), i32(lens), 64, 2)
+    check_attention(got, C.attend(ref, f64(q), offsets(n), lens, 64, 2), 128)
+    k, v = ba.cache_read(cache, i32([0, 96, 192]), i32([0, 0]), 192)
+    assert torch.equal(k[:96], k[96:]) and torch.equal(v[:96], v[96:])
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_rows_behind_the_last_sequence_of_a_padded_batch(rows):
+    """Tensors longer than the offsets say: what belongs to the rest stays as it was, split or not."""
+    lens, spare = [6000], 5
+    cache, ref, rng = build(rows, [6000 + rows], 1, 64, 16, extra_pages=3, spare=2)
+    offs = i32([0, rows])
+    q = queries(rng, rows + spare, 1, 64).cuda()
+    mean = torch.from_numpy(rng.normal(size=(ref.k.shape[0], 1, 64))).float().cuda()
+    for block, split in ((1 << 20, True), (64, False)):
+        assert (ba.ba_cache_fwd_workspace_size(cache, ba.make_problem(q, offs), block, 1) > 0) or not split
+        out = torch.full_like(q, 9.0)
+        lse = torch.full((1, rows + spare), 9.0, device="cuda")
+        ba.cache_attention_fwd(cache, q, offs, i32(lens), block, 1, out=out, lse=lse)
+        assert torch.all(out[rows:] == 9.0) and torch.all(lse[:, rows:] == 9.0)
+        alone = ba.cache_attention_fwd(cache, q[:rows].contiguous(), offs, i32(lens), block, 1)
+        assert torch.isfinite(alone[1]).all() and torch.allclose(alone[1], lse[:, :rows], atol=1e-4)
+    mask = torch.full((rows + spare, 1, -(-ref.table.shape[1] // 32)), 9, dtype=torch.int32, device="cuda")
+    ba.cache_select(cache, q, offs, i32(lens), mean, 64, 1, 3, page_mask=mask)
+    assert torch.all(mask[rows:] == 9)
+    want = C.select(ref, f64(q[:rows]), [0, rows], lens, f64(mean), 64, 1, 3)
+    assert np.array_equal(mask[:rows].cpu().numpy(), C.words(want))
+    k, v = (torch.full((rows + spare, 1, 64), 9.0, device="cuda") for _ in "kv")
+    ba.cache_read(cache, offs, i32(lens), rows + spare, k=k, v=v)
+    assert torch.all(k[rows:] == 9.0) and torch.all(v[rows:] == 9.0) and not torch.any(k[:rows] == 9.0)
+    before = cache.k.clone()
+    ba.cache_write(cache, k, v, offs, i32(lens))
+    assert torch.equal(cache.k.view(torch.float8_e4m3fn).float(), before.view(torch.float8_e4m3fn).float())
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
+def test_nan_in_a_value_column_of_many_rows():
+    lens = [100]
+    cache, ref, rng = build(4, [140], 1, 128, 16)
+    tree, pos = tree_case(rng, lens, [40], "candidates")
+    q = queries(rng, 40, 1, 128)
+    args = (q.cuda(), i32([0, 40]), i32(lens), 32, 2)
+    kw = dict(positions=i32(pos), tree_mask=i32(tree))
+    clean = ba.cache_attention_fwd(cache, *args, **kw)
+    page, at = ref.slot(0, 103)
+    cache.v[page, 0, at, 77] = 0x7F
+    got = ba.cache_attention_fwd(cache, *args, **kw)
+    same = torch.ones_like(clean[0], dtype=torch.bool)
+    same[3, 0, 77] = False
+    assert torch.equal(got[0][same], clean[0][same]) and torch.equal(got[1], clean[1])
+    assert torch.isnan(got[0][3, 0, 77])
+
+
+def test_element_offsets_past_32_bits_of_bulk_copies():
+    pages, size, heads, D = 70000, 128, 4, 128
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32)
+    cache = ba.HistoryCache.empty(pages, size, heads, D, table.cuda())
+    rng = np.random.default_rng(2)
+    x = [torch.from_numpy(rng.normal(size=(230, heads, D))).to(torch.bfloat16).cuda() for _ in "kv"]
+    ba.cache_write(cache, x[0], x[1], i32([0, 230]), i32([0]))
+    last = [t[pages - 2:].cpu().numpy() for t in (cache.k, cache.v, cache.k_scales, cache.v_scales)]
+    ref = C.Cache(*last, np.array([[1, 0]]))
+    q = queries(rng, 30, heads, D)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32([0, 30]), i32([200]), 1 << 20, 1)
+    check_attention(got, C.attend(ref, f64(q), [0, 30], [200], 1 << 20, 1), D)
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
 # ------------------------------------------------------------- used together ---
 
 def test_a_history_served_step_by_step():
@@ -635,6 +784,37 @@ def test_two_streams_at_once():
     ba.cache_attention_fwd(cache, q, offs, lens, 1 << 20, 1, out=out, lse=lse, workspace=ws, stream=streams[0])
     streams[0].synchronize()
     assert torch.equal(out, want[0][0])
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_two_graphs_share_a_workspace(rows):
+    """Two captured calls over different caches and one workspace, replayed in turn on a stream of their own."""
+    made = []
+    for seed in (rows, rows + 50):
+        cache, _, rng = build(seed, [4000 + rows], 1, 128, 64)
+        q = queries(rng, rows, 1, 128).cuda()
+        made.append((cache, q, i32([0, rows]), i32([4000])))
+    want = [ba.cache_attention_fwd(*m, 1 << 20, 1) for m in made]
+    need = max(ba.ba_cache_fwd_workspace_size(m[0], ba.make_problem(m[1], m[2]), 1 << 20, 1) for m in made)
+    assert need > 0
+    ws = ba.workspace_for(need, "cuda")
+    outs = [(torch.empty_like(m[1]), torch.empty((1, rows), device="cuda")) for m in made]
+    graphs = []
+    torch.cuda.synchronize()
+    for m, (out, lse) in zip(made, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ba.cache_attention_fwd(*m, 1 << 20, 1, out=out, lse=lse, workspace=ws)
+        graphs.append(graph)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            for (out, lse), graph in zip(outs, graphs):
+                out.zero_()
+                graph.replay()
+        side.synchronize()
+        for (out, lse), w in zip(outs, want):
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
 
 
 def test_the_binding_refuses_what_does_not_fit():
