@@ -644,25 +644,55 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
                 bool fine = fabsf(low) < INFINITY && k.count(score_key(-INFINITY)) == k.count(1);
                 cut = fine ? score_key(low) : 1u;
                 if (k.count(cut) > topk) {
-                    // some stay in doubt: those above the band certainly in (the largest key), below
-                    // it out (0), in it by their float64 score. From the last pages down, since a
-                    // 64-bit key covers two of the 32-bit ones.
-                    const uint32_t above = fine ? score_key(tau + 2.02f * bound) : ~0u;
+                    // some stay in doubt: those above the band are in, below it out, in it ranked by
+                    // their float64 scores
+                    const uint32_t above = fine ? score_key(tau + 2.02f * bound) : ~0u - 1;
+                    const int32_t sure = k.count(above + 1), doubts = k.count(cut) - sure;
+                    double qd[D / 32];
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) qd[i] = q_sum(r, i * 32 + lane);
+                    auto score = [&](int32_t page) { // over the warp
+                        const float *mean = summaries + (int64_t(cache_page(c, b, page)) * c.kv_heads + h) * D + lane;
+                        double s = 0.0;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) s = fma(qd[i], double(__ldg(mean + i * 32)), s);
+#pragma unroll
+                        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                        return score_key(s);
+                    };
+                    if (doubts <= 32) { // a lane each, in the pages' order
+                        uint64_t mine = 0;
+                        int32_t page = 0, got = 0;
+                        for (int32_t p0 = 0; p0 < most && got < doubts; p0 += 32) {
+                            const uint32_t x = p0 + lane < most ? key32[p0 + lane] : 0;
+                            uint32_t doubt = __ballot_sync(0xffffffffu, x >= cut && x <= above);
+                            for (; doubt; doubt &= doubt - 1, ++got) {
+                                const int32_t p = p0 + __ffs(doubt) - 1;
+                                const uint64_t y = score(p);
+                                if (lane == got) mine = y, page = p;
+                            }
+                        }
+                        int32_t rank = 0;
+                        for (int32_t j = 0; j < doubts; ++j) {
+                            const uint64_t y = __shfl_sync(0xffffffffu, mine, j);
+                            rank += y > mine || (y == mine && j < lane);
+                        }
+                        if (lane < doubts) key32[page] = rank < topk - sure ? ~0u : 0;
+                        __syncwarp();
+                        write_bits(key32, most, above + 1, most, dst, words);
+                        return;
+                    }
+                    // more: their scores' keys in place of the float32 ones, the largest for those above and
+                    // 0 for those below. From the last pages down, since a 64-bit key covers two of the others.
                     for (int32_t p0 = (most - 1) / 32 * 32; p0 >= 0; p0 -= 32) {
                         const int32_t p = p0 + lane;
                         const uint32_t x = p < most ? key32[p] : 0;
-                        uint64_t y = x > above && fine ? ~uint64_t(0) : 0;
-                        uint32_t doubt = __ballot_sync(0xffffffffu, y == 0 && x != 0 && x >= cut);
-                        while (doubt) {
+                        uint64_t y = x > above ? ~uint64_t(0) : 0;
+                        uint32_t doubt = __ballot_sync(0xffffffffu, x >= cut && x <= above);
+                        for (; doubt; doubt &= doubt - 1) {
                             const int at_lane = __ffs(doubt) - 1;
-                            doubt &= doubt - 1;
-                            const int32_t page = cache_page(c, b, p0 + at_lane);
-                            const float *mean = summaries + (int64_t(page) * c.kv_heads + h) * D;
-                            double s = 0.0;
-                            for (int d = lane; d < D; d += 32) s = fma(q_sum(r, d), double(__ldg(mean + d)), s);
-#pragma unroll
-                            for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                            if (lane == at_lane) y = score_key(s);
+                            const uint64_t z = score(p0 + at_lane);
+                            if (lane == at_lane) y = z;
                         }
                         __syncwarp();
                         if (p < most) key64[p] = y;
