@@ -471,38 +471,61 @@ __device__ __forceinline__ void write_bits(const K *key, int32_t most, K edge, i
     }
 }
 
-// a warp a row for the final choice, and four for one row's scores
+// a warp a row for the final choice, and four for one row
 __host__ __device__ constexpr int select_warps(int rows) { return rows > 4 ? rows : 4; }
-constexpr int kMeanStride = 36; // floats a page in a warp's staged piece: 32 columns, and 4 so that
-                                // eight lanes' 16-byte reads of eight pages meet all banks
+
+__device__ __forceinline__ void select_mma(float (&c)[4], const uint32_t (&a)[4], uint2 b)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+
+// Two values as bf16 and what is left of them, as bf16 too: a = hi + lo up to 2^-16 |a|.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
 
 } // namespace
 
 // Scores of the candidate pages for kRows rows of one (sequence, key/value head), then the
 // topk of each. Which of two pages wins is decided by the scores in float64 (the products of
 // bf16 queries and float32 means are exact there, the sums off by some 2^-53, so the choice
-// does not hang on the order of summation), but few pages need one: all scores are formed in
-// float32, off by at most E = (D + 4) 2^-24 sum |q| max |mean| (D products and additions, the
-// rounding of q's sum over the group; 1.01 for E's own roundings), so with tau the topk-th
-// largest of them, pages above tau + 2 E are in, pages below tau - 2 E out, and only when more
-// than topk pages reach tau - 2 E are those in between scored again in float64. (All in
-// float64: 50 us where this takes less than half; DFMA chains, not bandwidth, were the bound.)
+// does not hang on the order of summation), but few pages need one: all scores are formed
+// less exactly, off by at most E, so with tau the topk-th largest of them, pages above tau + 2 E
+// are in, pages below tau - 2 E out, and only when more than topk pages reach tau - 2 E are
+// those in between scored again in float64. (All in float64: 50 us for the scores alone in the
+// case below; DFMA chains, not bandwidth, were the bound.)
 //
-// A warp takes 32 pages, a lane one of them: 32 columns of their means at a time go through
-// shared memory (read from HBM in whole lines, the next piece's loads under way), and the
-// lane's kRows sums need no exchange with other lanes.
+// The scores are warp-wide MMAs of 16 pages by 8 rows. Means and sums of queries are split in
+// two bf16 each, m = m1 + m2 and q = q1 + q2 up to 2^-16 of their size, and m1 q1 + m2 q1 + m1 q2
+// are added up in float32 (q2 is 0 for a group of one head, whose queries are bf16 already).
+// With A = sum |q| and M = max |mean|, each MMA's 16 products and its sum so far, all below A M,
+// lose at most 18 2^-23 A M (cut, not rounded), the splits 2^-16 A M for each product of rests
+// that is left out, the rounding of q to float32 2^-24 A M: E is their sum, 1.01 for E's own
+// roundings, and an absolute part for what underflows. A lane's four consecutive columns of
+// its two pages are its columns of an MMA step, so the means go from memory to the MMAs
+// through registers alone. (Float32 on the CUDA cores, one page a lane, means through shared
+// memory and a tighter band: 45 us where this takes 28, for 8 trees of 17 to 64 rows over
+// 16,000 to 33,000 events in 64-slot pages, 8 heads of 128, the 32 best pages.) Bound by the
+// chain of a block's latencies: offsets, page numbers, means, then the choice, some 8 us of
+// the 28. Three blocks of eight rows an SM, at the price of a few spilled registers: with two
+// 32 us. Rows go to blocks of four warps one by one (eight: 15.5 for 14.0 us, 64 histories).
 template <int D, int kRows>
-__global__ void __launch_bounds__(select_warps(kRows) * 32)
+__global__ void __launch_bounds__(select_warps(kRows) * 32, kRows > 1 ? 3 : 4)
     cache_select_kernel(const CacheView c, const CacheQuery q, const float *__restrict__ summaries, int32_t topk,
                         uint32_t *__restrict__ page_mask)
 {
-    constexpr int kPieces = D / 32, kWarps = select_warps(kRows);
+    constexpr int kSteps = D / 16, kWarps = select_warps(kRows);
     extern __shared__ __align__(16) uint64_t keys[]; // [kRows][max_pages]: float32 keys in a row's first half
-    __shared__ __align__(16) float qs[kRows][D];     // the rows' query sums over the group
-    __shared__ __align__(16) float means[kWarps][32 * kMeanStride];
+    __shared__ uint2 q_hi[kSteps][32], q_lo[kSteps][32]; // the rows' sums over the group, as MMA fragments
+    __shared__ float q_abs[kSteps][8];               // sums of their magnitudes
     __shared__ int32_t cands[kRows];
     __shared__ uint32_t max_mean;                    // largest |mean| (its bits)
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int32_t h = blockIdx.y;
     // the sequence and its tile of kRows rows: tiles are numbered floor(offs[b] / kRows) + b
     // (tiles of one row by their row)
@@ -539,82 +562,83 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
     if (threadIdx.x == 0) max_mean = 0;
     const __nv_bfloat16 *const q_first = q.q + ((int64_t(q0) + t0) * c.kv_heads + h) * q.group * D;
     const int64_t q_row = int64_t(c.kv_heads) * q.group * D;
-    // column d of row r's sum over the group
-    auto q_sum = [&](int r, int d) {
-        double s = 0.0;
-        for (int32_t g = 0; g < q.group; ++g) s += double(__bfloat162float(q_first[r * q_row + g * D + d]));
-        return s;
+    // columns d .. d + 3 of row r's sum over the group
+    auto q_sum = [&](int r, int d, double (&s)[4]) {
+        s[0] = s[1] = s[2] = s[3] = 0.0;
+        const uint2 *src = reinterpret_cast<const uint2 *>(q_first + r * q_row + d);
+#pragma unroll 4
+        for (int32_t x = 0; x < q.group; ++x) {
+            const uint2 w = __ldg(src + x * (D / 4));
+            s[0] += double(__uint_as_float(w.x << 16));
+            s[1] += double(__uint_as_float(w.x & 0xffff0000u));
+            s[2] += double(__uint_as_float(w.y << 16));
+            s[3] += double(__uint_as_float(w.y & 0xffff0000u));
+        }
     };
-    for (int x = threadIdx.x; x < kRows * D; x += kWarps * 32)
-        qs[x / D][x % D] = t0 + x / D < n ? float(q_sum(x / D, x % D)) : 0.f;
+    for (int x = warp; x < kSteps; x += kWarps) { // (lane: row g, columns 16 x + 4 t4 ..)
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (g < kRows && t0 + g < n) {
+            double s[4];
+            q_sum(g, 16 * x + 4 * t4, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = float(s[i]);
+        }
+        uint2 hi, lo;
+        split_bf16x2(f[0], f[1], hi.x, lo.x);
+        split_bf16x2(f[2], f[3], hi.y, lo.y);
+        q_hi[x][lane] = hi;
+        q_lo[x][lane] = lo;
+        float a = fabsf(f[0]) + fabsf(f[1]) + (fabsf(f[2]) + fabsf(f[3]));
+        a += __shfl_xor_sync(0xffffffffu, a, 1);
+        a += __shfl_xor_sync(0xffffffffu, a, 2);
+        if (t4 == 0) q_abs[x][g] = a;
+    }
     __syncthreads();
     int32_t most = 0;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) most = max(most, cands[r]);
 
-    float *const piece = means[warp];
+    const bool grouped = q.group > 1;
     float largest = 0.f;
-    for (int32_t p0 = warp * 32; p0 < most; p0 += kWarps * 32) {
+    const float *const head = summaries + h * D + t4 * 4;
+    for (int32_t p0 = warp * 16; p0 < most; p0 += kWarps * 16) {
         int32_t id = -1;
-        if (p0 + lane < most) {
+        if (lane < 16 && p0 + lane < most) {
             id = cache_page(c, b, p0 + lane);
             if (id < 0) cache_range_error(c);
         }
-        // lane 8 x + y loads 16 bytes, columns 4 y .. 4 y + 3 of the piece, of pages x, x + 4, ...
-        // (page 0's where there is none: a choice after the load would wait for it here)
-        float4 next[8];
-        uint32_t from[8];
+        float4 w[2][kSteps]; // of pages p0 + g, p0 + g + 8
+        int32_t from[2];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            from[u] = uint32_t(max(__shfl_sync(0xffffffffu, id, 4 * u + (lane >> 3)), 0));
-        const float *const head = summaries + h * D + (lane & 7) * 4;
-        auto load = [&](int part) {
+        for (int i = 0; i < 2; ++i) {
+            from[i] = __shfl_sync(0xffffffffu, id, g + 8 * i);
+            const float4 *src = reinterpret_cast<const float4 *>(head + int64_t(from[i]) * (c.kv_heads * D));
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                next[u] = __ldg(reinterpret_cast<const float4 *>(head + uint64_t(from[u]) * uint32_t(c.kv_heads * D) +
-                                                                 part * 32));
-        };
-        float here = 0.f; // largest |mean| of this lane's page
-        float2 acc[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) acc[r] = make_float2(0.f, 0.f);
-        load(0);
-#pragma unroll 1
-        for (int part = 0; part < kPieces; ++part) {
-            __syncwarp();
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4 *>(piece + (4 * u + (lane >> 3)) * kMeanStride + 4 * (lane & 7)) = next[u];
-            __syncwarp();
-            if (part + 1 < kPieces) load(part + 1);
-            // a step's operands are read while the previous step's are used
-            float4 m = *reinterpret_cast<const float4 *>(piece + lane * kMeanStride), a[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) a[r] = *reinterpret_cast<const float4 *>(&qs[r][part * 32]);
-#pragma unroll
-            for (int d = 0; d < 32; d += 4) {
-                const int e = (d + 4) % 32;
-                const float4 m2 = *reinterpret_cast<const float4 *>(piece + lane * kMeanStride + e);
-                float4 a2[kRows];
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) a2[r] = *reinterpret_cast<const float4 *>(&qs[r][part * 32 + e]);
-                here = fmax3(here, fabsf(m.x), fabsf(m.y));
-                here = fmax3(here, fabsf(m.z), fabsf(m.w));
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) acc[r] = ffma2(make_float2(a[r].x, a[r].y), make_float2(m.x, m.y), acc[r]);
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) acc[r] = ffma2(make_float2(a[r].z, a[r].w), make_float2(m.z, m.w), acc[r]);
-                m = m2;
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) a[r] = a2[r];
-            }
+            for (int x = 0; x < kSteps; ++x)
+                w[i][x] = from[i] >= 0 ? __ldg(src + 4 * x) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (id >= 0) largest = fmaxf(largest, here);
-        if (p0 + lane < most) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
-                reinterpret_cast<uint32_t *>(keys + int64_t(r) * c.max_pages)[p0 + lane] =
-                    p0 + lane < cands[r] && id >= 0 ? score_key(acc[r].x + acc[r].y) : 0;
+        for (int x = 0; x < kSteps; ++x) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                largest = fmax3(largest, fabsf(w[i][x].x), fabsf(w[i][x].y));
+                largest = fmax3(largest, fabsf(w[i][x].z), fabsf(w[i][x].w));
+                split_bf16x2(w[i][x].x, w[i][x].y, hi[i], lo[i]);
+                split_bf16x2(w[i][x].z, w[i][x].w, hi[2 + i], lo[2 + i]);
+            }
+            const uint2 b_hi = q_hi[x][lane];
+            select_mma(acc, hi, b_hi);
+            select_mma(acc, lo, b_hi);
+            if (grouped) select_mma(acc, hi, q_lo[x][lane]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = 2 * t4 + (e & 1), p = p0 + g + 8 * (e >> 1);
+            if (r < kRows && p < most)
+                reinterpret_cast<uint32_t *>(keys + int64_t(r) * c.max_pages)[p] =
+                    p < cands[r] && from[e >> 1] >= 0 ? score_key(acc[e]) : 0;
         }
     }
     const uint32_t most_mean = warp_max(__float_as_uint(largest));
@@ -627,12 +651,14 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
         uint64_t *const key64 = keys + int64_t(r) * c.max_pages;
         uint32_t *const key32 = reinterpret_cast<uint32_t *>(key64);
         uint32_t *const dst = page_mask + ((int64_t(q0) + t0 + r) * c.kv_heads + h) * words;
-        float bound = 0.f; // sum |q|
-        for (int d = lane; d < D; d += 32) bound += fabsf(qs[r][d]);
+        float bound = 0.f; // sum |q|, then E
 #pragma unroll
-        for (int m = 16; m; m >>= 1) bound += __shfl_xor_sync(0xffffffffu, bound, m);
-        // (an absolute part for products that underflow)
-        bound = fmaf(bound * __uint_as_float(max_mean), (D + 4) * 1.01f / 16777216.f, 1e-42f);
+        for (int x = 0; x < kSteps; ++x) bound += q_abs[x][r];
+        const float least = (bound + D * __uint_as_float(max_mean) + D) * 0x1p-120f;
+        bound = fmaf(bound * __uint_as_float(max_mean),
+                     1.01f * (grouped ? 3 * kSteps * 18 * 0x1p-23f + 3 * 0x1p-16f + 0x1p-24f
+                                      : 2 * kSteps * 18 * 0x1p-23f + 0x1p-16f),
+                     least);
         uint32_t cut = 1; // pages at or above it are taken, if they are at most topk
         {
             const Keys<uint32_t, kHeld> k(key32, most);
@@ -648,29 +674,40 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
                     // their float64 scores
                     const uint32_t above = fine ? score_key(tau + 2.02f * bound) : ~0u - 1;
                     const int32_t sure = k.count(above + 1), doubts = k.count(cut) - sure;
-                    double qd[D / 32];
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) qd[i] = q_sum(r, i * 32 + lane);
-                    auto score = [&](int32_t page) { // over the warp
-                        const float *mean = summaries + (int64_t(cache_page(c, b, page)) * c.kv_heads + h) * D + lane;
+                    // of four pages at once: eight lanes one
+                    auto score = [&](int32_t page) {
                         double s = 0.0;
+                        if (page >= 0) {
+                            const float *mean = summaries + (int64_t(cache_page(c, b, page)) * c.kv_heads + h) * D;
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) s = fma(qd[i], double(__ldg(mean + i * 32)), s);
+                            for (int i = 0; i < D / 32; ++i) {
+                                const int d = 32 * i + 4 * (lane & 7);
+                                const float4 m = __ldg(reinterpret_cast<const float4 *>(mean + d));
+                                double x[4];
+                                q_sum(r, d, x);
+                                s = fma(x[0], double(m.x), s);
+                                s = fma(x[1], double(m.y), s);
+                                s = fma(x[2], double(m.z), s);
+                                s = fma(x[3], double(m.w), s);
+                            }
+                        }
 #pragma unroll
-                        for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                        for (int m = 4; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
                         return score_key(s);
                     };
                     if (doubts <= 32) { // a lane each, in the pages' order
                         uint64_t mine = 0;
-                        int32_t page = 0, got = 0;
+                        int32_t page = -1, got = 0;
                         for (int32_t p0 = 0; p0 < most && got < doubts; p0 += 32) {
                             const uint32_t x = p0 + lane < most ? key32[p0 + lane] : 0;
-                            uint32_t doubt = __ballot_sync(0xffffffffu, x >= cut && x <= above);
-                            for (; doubt; doubt &= doubt - 1, ++got) {
-                                const int32_t p = p0 + __ffs(doubt) - 1;
-                                const uint64_t y = score(p);
-                                if (lane == got) mine = y, page = p;
-                            }
+                            const bool doubt = x >= cut && x <= above;
+                            for (uint32_t left = __ballot_sync(0xffffffffu, doubt); left; left &= left - 1, ++got)
+                                if (lane == got) page = p0 + __ffs(left) - 1;
+                        }
+                        for (int32_t j = 0; j < doubts; j += 4) {
+                            const int32_t at = __shfl_sync(0xffffffffu, page, (j + (lane >> 3)) & 31);
+                            const uint64_t y = __shfl_sync(0xffffffffu, score(at), 8 * (lane & 3));
+                            if (lane >= j && lane < j + 4) mine = y;
                         }
                         int32_t rank = 0;
                         for (int32_t j = 0; j < doubts; ++j) {
@@ -689,10 +726,19 @@ __global__ void __launch_bounds__(select_warps(kRows) * 32)
                         const uint32_t x = p < most ? key32[p] : 0;
                         uint64_t y = x > above ? ~uint64_t(0) : 0;
                         uint32_t doubt = __ballot_sync(0xffffffffu, x >= cut && x <= above);
-                        for (; doubt; doubt &= doubt - 1) {
-                            const int at_lane = __ffs(doubt) - 1;
-                            const uint64_t z = score(p0 + at_lane);
-                            if (lane == at_lane) y = z;
+                        while (doubt) {
+                            int32_t mine = -1; // this lane's four pages' first, second, ... by its eight
+                            uint32_t now = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (!doubt) break;
+                                if (lane >> 3 == i) mine = p0 + __ffs(doubt) - 1;
+                                now |= doubt & -doubt;
+                                doubt &= doubt - 1;
+                            }
+                            const uint64_t z = __shfl_sync(0xffffffffu, score(mine),
+                                                           8 * (__popc(now & ((1u << lane) - 1)) & 3));
+                            if ((now >> lane) & 1u) y = z;
                         }
                         __syncwarp();
                         if (p < most) key64[p] = y;
@@ -727,8 +773,7 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
 {
     auto kern = cache_select_kernel<D, kRows>;
     const size_t smem = size_t(kRows) * c.max_pages * 8;
-    constexpr size_t kStatic = (select_warps(kRows) * 32 * kMeanStride + kRows * (D + 1)) * 4 + 64; // at most
-    if (kStatic + smem > 48 * 1024) {
+    if (smem > 43 * 1024) { // (beside up to 5 KB of static shared memory)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
