@@ -267,6 +267,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     FwdTile t;
     if (!find_tile(p, blockIdx.x, kMmaRows, t)) return;
     const int active = (t.rows + 31) / 32; // softmax warps with rows
+    if (split > 0 && int64_t(split) * p.chunk >= t.end) { // a split past the history's end
+        if (tid < t.rows)
+            p.part_ml[int64_t(split) * p.q.rows * p.c.kv_heads * p.q.group + out_row(p, t, h, t.row0 + tid)] =
+                make_float2(-INFINITY, 0.f);
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
