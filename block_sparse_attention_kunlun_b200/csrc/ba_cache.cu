@@ -68,7 +68,8 @@ __device__ __forceinline__ uint32_t div_heads(uint32_t x, uint32_t d, uint32_t m
 // 2^9; what underflows is far below E4M3's smallest value), so the conversion to E4M3 is the
 // only rounding. fmaxf drops NaN: a NaN leaves its block's scale alone and becomes E4M3's NaN;
 // an infinity gives e = 120 and the largest code.
-// Bound by HBM for many rows (each thread has kBatch loads under way), by the launch for few.
+// Bound by HBM for many rows (each thread has kBatch loads under way): whole jagged histories
+// of 540,000 rows of 8 heads of 128 in bf16, 3.3 GB, in 561 us, 5.9 TB/s. By the launch for few.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_write_kernel(const CacheView c, const T *__restrict__ k, const T *__restrict__ v,
@@ -137,7 +138,8 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // D / 16 lanes hold a (row, head), sixteen values each: 16 bytes of codes in, 32 (bf16) or 64
 // bytes out. A bf16 result is exact (four significant bits) unless it falls below bf16's
-// normal range. Bound by HBM.
+// normal range. Bound by HBM: 65,000 rows of 8 heads of 128 as bf16, 0.41 GB, in 71 us, 5.7
+// TB/s; as float32 (0.085 GB) 18 us, with 16-byte stores 25.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_read_kernel(const CacheView c, const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts,
@@ -270,7 +272,9 @@ cudaError_t launch_cache_read(const CacheView &c, bool f32, const int32_t *row_o
 // One warp per (page, head): its slots are page_size * head_dim consecutive bytes, read 16
 // bytes a lane, eight loads at a time; each lane sums its sixteen columns over its rows in
 // float32 and the lanes that share columns are added at the end. The pages of a (sequence,
-// head) are dealt to `share` warps. Bound by HBM for many pages, by one page's latency for few.
+// head) are dealt to `share` warps. Bound by one page's latency for few pages (10 us for one
+// of each of 256 histories, most of it the launch); for many by HBM and by the shuffles at each
+// page's end: 0.29 GB of keys in 60 us, 4.9 TB/s.
 template <int D>
 __global__ void __launch_bounds__(128)
     cache_summarize_kernel(const CacheView c, const int32_t *__restrict__ starts, const int32_t *__restrict__ ends,
