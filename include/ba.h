@@ -377,7 +377,8 @@ ba_status ba_fwd_noalloc(const ba_problem *p, const void *q, const void *k, cons
  *  - status: DEVICE int32 word or NULL. The calls only ever set bits in it;
  *    the caller zeroes it. After a call met a slot past max_pages or without
  *    a page (skipped: nothing outside the pools is read or written),
- *    ba_device_status(status, stream) returns BA_ERR_INVALID_ARG.
+ *    ba_device_status(status, stream) returns BA_ERR_INVALID_ARG; after a
+ *    kernel gave up waiting, BA_ERR_TIMEOUT. With NULL neither is reported.
  *  - page_size 16, 32, 64 or 128; head_dim 64 or 128 (else
  *    BA_ERR_UNSUPPORTED); kv_heads <= 65535; max_pages * page_size <=
  *    2^30.
