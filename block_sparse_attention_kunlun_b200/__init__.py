@@ -940,6 +940,8 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
         if tree_mask.dim() != 2:
             raise ValueError("tree_mask must be [rows, words]")
         words = tree_mask.shape[1]
+        if words < 1:
+            raise ValueError("tree_mask must have a word a row")
         named.append(("tree_mask", tree_mask, torch.int32, (rows, words)))
     if page_mask is not None:
         named.append(("page_mask", page_mask, torch.int32, (rows, cache._row[0], cache._words)))
@@ -949,6 +951,8 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
     ref = ctypes.byref(prob)
     if workspace is None:
         workspace = workspace_for(_load().ba_cache_fwd_workspace_size(cache._ref, ref, block, window), q.device)
+    elif workspace.get_device() != cache._index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
     st = _load().ba_cache_fwd(cache._ref, ref, q.data_ptr(), q_offsets.data_ptr(), lens.data_ptr(), _ptr(positions),
                               _ptr(tree_mask), words, _ptr(page_mask), block, window, out.data_ptr(), lse.data_ptr(),
                               workspace.data_ptr(), workspace.numel() * workspace.element_size(), _on(cache, stream))

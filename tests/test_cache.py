@@ -575,6 +575,25 @@ def test_values_and_keys_of_any_scale(rows, D):
                     more=3 * 2.0 ** -118 * np.abs(seen).sum(axis=0))
 
 
+@pytest.mark.parametrize("rows", ROWS[1:])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_row_that_is_not_finite_reaches_no_other(rows, value):
+    lens = [400]
+    cache, ref, rng = build(rows, [400 + rows], 1, 128, 64)
+    q = queries(rng, rows, 1, 128)
+    mask = C.words(rng.random((rows, 1, ref.table.shape[1])) < 0.5)
+    args = (i32([0, rows]), i32(lens), 64, 2)
+    clean = ba.cache_attention_fwd(cache, q.cuda(), *args, page_mask=i32(mask))
+    mean = torch.from_numpy(rng.normal(size=(ref.k.shape[0], 1, 128))).float().cuda()
+    chosen = ba.cache_select(cache, q.cuda(), *args[:2], mean, 64, 1, 2)
+    q[2, 0, 7] = value
+    got = ba.cache_attention_fwd(cache, q.cuda(), *args, page_mask=i32(mask))
+    rest = [t for t in range(rows) if t != 2]
+    assert torch.equal(got[0][rest], clean[0][rest]) and torch.equal(got[1][:, rest], clean[1][:, rest])
+    assert torch.isnan(got[0][2]).all()
+    assert torch.equal(ba.cache_select(cache, q.cuda(), *args[:2], mean, 64, 1, 2)[rest], chosen[rest])
+
+
 @pytest.mark.parametrize("rows", ROWS)
 def test_sequences_that_share_pages(rows):
     """Two sequences on the same pages of a common beginning, with pages of their own after it."""
@@ -832,7 +851,8 @@ def test_the_binding_refuses_what_does_not_fit():
         with pytest.raises(ValueError):
             ba.cache_select(cache, a["q"], a["offs"], a["lens"], torch.zeros((cache.k.shape[0], 2, 64), device="cuda"),
                             16, 1, 2)
-    for kw in (dict(positions=i32([1])), dict(tree_mask=i32([1, 1])), dict(page_mask=i32([[1], [1]])),
+    for kw in (dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)), dict(tree_mask=i32([[], []])),
+               dict(positions=i32([1])), dict(tree_mask=i32([1, 1])), dict(page_mask=i32([[1], [1]])),
                dict(out=q.float()), dict(lse=torch.zeros(2, 2, device="cuda"))):
         with pytest.raises(ValueError):
             ba.cache_attention_fwd(cache, q, offs, lens, 16, 1, **kw)
