@@ -272,9 +272,10 @@ cudaError_t launch_cache_read(const CacheView &c, bool f32, const int32_t *row_o
 // One warp per (page, head): its slots are page_size * head_dim consecutive bytes, read 16
 // bytes a lane, eight loads at a time; each lane sums its sixteen columns over its rows in
 // float32 and the lanes that share columns are added at the end. The pages of a (sequence,
-// head) are dealt to `share` warps. Bound by one page's latency for few pages (10 us for one
-// of each of 256 histories, most of it the launch); for many by HBM and by the shuffles at each
-// page's end: 0.29 GB of keys in 60 us, 4.9 TB/s.
+// head) are dealt to `share` warps, as many as the GPU holds at 128 registers a thread. Bound by
+// one page's latency for few pages (9 us for one of each of 256 histories, most of it the
+// launch); for many by HBM: 0.29 GB of keys in 52 us, 5.6 TB/s (60 with each batch loaded after
+// the one before it was summed; 112 squeezed into 96 registers for more warps).
 template <int D>
 __global__ void __launch_bounds__(128)
     cache_summarize_kernel(const CacheView c, const int32_t *__restrict__ starts, const int32_t *__restrict__ ends,
@@ -293,27 +294,40 @@ __global__ void __launch_bounds__(128)
     const int32_t loads = (1 << c.page_shift) / kRows; // of a page: 2 .. 32
     const int col = lane % kLanes;
     const float inv = 1.f / float(1 << c.page_shift); // a power of two
-    for (int32_t pi = first + part; pi < stop; pi += share) {
-        const int32_t id = cache_page(c, b, pi);
-        if (id < 0) {
+    // this warp's pages: the number of the next one, and the next batch's loads, are under way
+    // while a batch is summed
+    auto page_at = [&](int32_t &pi) { // the next page that has a number, from pi on
+        for (; pi < stop; pi += share) {
+            const int32_t id = cache_page(c, b, pi);
+            if (id >= 0) return id;
             if (lane == 0) cache_range_error(c);
-            continue;
         }
+        return -1;
+    };
+    uint4 w[kBatch], w2[kBatch];
+    uint32_t code[kBatch], code2[kBatch];
+    auto load = [&](int32_t id, int32_t u0, uint4 (&x)[kBatch], uint32_t (&y)[kBatch]) {
         const int64_t row0 = cache_row(c, id, h, 0);
         const uint4 *src = reinterpret_cast<const uint4 *>(c.k + row0 * D) + lane;
         const uint8_t *sc = c.k_scales + (row0 + lane / kLanes) * (D / 32) + col / 2;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (u0 + u < loads) {
+                x[u] = __ldg(src + (u0 + u) * 32);
+                y[u] = __ldg(sc + (u0 + u) * kRows * (D / 32));
+            }
+    };
+    int32_t pi = first + part, id = page_at(pi);
+    if (id >= 0) load(id, 0, w, code);
+    while (id >= 0) {
+        pi += share;
+        const int32_t next = page_at(pi);
         float2 acc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = make_float2(0.f, 0.f);
         for (int32_t u0 = 0; u0 < loads; u0 += kBatch) {
-            uint4 w[kBatch];
-            uint32_t code[kBatch];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u0 + u < loads) {
-                    w[u] = __ldg(src + (u0 + u) * 32);
-                    code[u] = __ldg(sc + (u0 + u) * kRows * (D / 32));
-                }
+            if (u0 + kBatch < loads) load(id, u0 + kBatch, w2, code2);
+            else if (next >= 0) load(next, 0, w2, code2);
 #pragma unroll
             for (int u = 0; u < kBatch; ++u)
                 if (u0 + u < loads) {
@@ -324,6 +338,11 @@ __global__ void __launch_bounds__(128)
                     for (int i = 0; i < 8; ++i)
                         acc[i] = ffma2(e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), s2, acc[i]);
                 }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                w[u] = w2[u];
+                code[u] = code2[u];
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -340,15 +359,16 @@ __global__ void __launch_bounds__(128)
                 dst[i] = make_float4(acc[2 * i].x * inv, acc[2 * i].y * inv, acc[2 * i + 1].x * inv,
                                      acc[2 * i + 1].y * inv);
         }
+        id = next;
     }
 }
 
 cudaError_t launch_cache_summarize(const CacheView &c, const int32_t *starts, const int32_t *ends, float *summaries,
                                    int num_sms, cudaStream_t stream)
 {
-    // enough warps to fill the GPU whatever the number of (sequence, head) pairs
+    // as many warps as the GPU holds, whatever the number of (sequence, head) pairs
     const int64_t pairs = int64_t(c.batch) * c.kv_heads;
-    int64_t share = (int64_t(num_sms) * 32 + pairs - 1) / pairs;
+    int64_t share = (int64_t(num_sms) * 16 + pairs - 1) / pairs;
     if (share > c.max_pages) share = c.max_pages;
     const int64_t blocks = (pairs * share + 3) / 4;
     if (c.head_dim == 64)
