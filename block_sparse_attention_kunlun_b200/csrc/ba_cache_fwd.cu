@@ -24,6 +24,8 @@ namespace ba {
 namespace {
 
 constexpr int kSimtWarps = 4; // 128 threads: one a column at the end
+// blocks of the one-row kernel that an SM holds
+__host__ __device__ constexpr int simt_blocks(int head_dim) { return head_dim == 128 ? 5 : 7; }
 
 } // namespace
 
@@ -35,13 +37,15 @@ constexpr int kSimtWarps = 4; // 128 threads: one a column at the end
 // adds its 16 columns into its own running sum: each set of D / 16 lanes keeps the running
 // maximum and sum of the slots it has met, so the softmax needs no exchange inside the loop.
 // The sets and the warps are joined once at the end.
+// Values are on their way while scores are formed, the next slots' keys while values are added.
 // One event over the windows of 256 histories (8 heads of 128, up to 512 slots each, 0.20 GB):
-// 49 us, 4.1 TB/s, of which some 4 us go to the launch and, in each of a block's two rounds, 2
-// to 3 to finding its sequence and pages before the first keys are under way. 80 registers,
-// seven blocks an SM, so that one block's start-up hides behind the others' loads; splitting
-// the windows further (two, three parts) takes 56 and 61 us.
+// 47 us, 4.3 TB/s, of which some 4 us go to the launch and, in each of a block's rounds, 2
+// to 3 to finding its sequence and pages before the first keys are under way; over windows of
+// 4096 slots 223 us. Five blocks an SM (four, without a bound on registers: 50 and 228; six or
+// seven spill: 61 and 300); at D = 64, with half the codes a lane, seven (30 us; five 35).
+// Splitting the windows further (two, three parts) takes 12% and 21% more.
 template <int D>
-__global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const CacheFwd p)
+__global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D)) cache_fwd_simt_kernel(const CacheFwd p)
 {
     constexpr int kLanes = D / 16;      // lanes of a slot
     constexpr int kSets = 32 / kLanes;  // slots of a load
@@ -77,25 +81,55 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = make_float2(0.f, 0.f);
 
-    // 16 slots at `slot` on page `id`; vis: the slots that the row sees (kAll: all 16)
-    auto take = [&](int32_t slot, int32_t id, auto all_t, uint32_t vis) {
-        constexpr bool kAll = decltype(all_t)::value;
-        const int64_t row = cache_row(p.c, id, h, slot & ((1 << p.c.page_shift) - 1));
-        const uint4 *ks = reinterpret_cast<const uint4 *>(p.c.k + row * D) + lane;
-        const uint4 *vs = reinterpret_cast<const uint4 *>(p.c.v + row * D) + lane;
-        const int64_t srow = (row + set) * (D / 32) + col / 2;
-        uint4 kw[kU], vw[kU];
-        uint32_t kc[kU], vc[kU];
+    // walk of this warp's groups: 32 at a time are tested for being wanted
+    int32_t base = g0 - kSimtWarps * 32, id = -1;
+    uint32_t todo = 0;
+    auto next_group = [&](int32_t &slot, int64_t &row) -> bool {
+        while (!todo) {
+            base += kSimtWarps * 32;
+            if (base >= g1) return false;
+            const int32_t g = base + lane * kSimtWarps + warp, s0 = g * kGroup;
+            bool want = g < g1 && (s0 + kGroup > rv.ws || s0 + kGroup > t.len);
+            if (g < g1 && !want && p.page_mask) {
+                const int32_t page = s0 >> p.c.page_shift;
+                want = (__ldg(p.page_mask + ((int64_t(t.q0) + rv.tok) * p.c.kv_heads + h) * p.mask_words +
+                              (page >> 5)) >>
+                        (page & 31)) & 1u;
+            }
+            want = want && (s0 <= rv.pos || s0 + kGroup > t.len);
+            id = -1;
+            if (want) {
+                id = cache_page(p.c, t.b, s0 >> p.c.page_shift);
+                if (id < 0) cache_range_error(p.c);
+            }
+            todo = __ballot_sync(0xffffffffu, id >= 0);
+        }
+        const int x = __ffs(todo) - 1;
+        todo &= todo - 1;
+        slot = (base + x * kSimtWarps + warp) * kGroup;
+        row = cache_row(p.c, __shfl_sync(0xffffffffu, id, x), h, slot & ((1 << p.c.page_shift) - 1));
+        return true;
+    };
+    // a group's codes and scale codes of keys or values
+    auto load = [&](const uint8_t *codes, const uint8_t *scales, int64_t row, uint4 (&w)[kU], uint32_t (&c)[kU]) {
+        const uint4 *const src = reinterpret_cast<const uint4 *>(codes + row * D) + lane;
+        const uint8_t *const sc = scales + (row + set) * (D / 32) + col / 2;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            kw[u] = __ldg(ks + u * 32);
-            kc[u] = __ldg(p.c.k_scales + srow + u * kSets * (D / 32));
+            w[u] = __ldg(src + u * 32);
+            c[u] = __ldg(sc + u * kSets * (D / 32));
         }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            vw[u] = __ldg(vs + u * 32);
-            vc[u] = __ldg(p.c.v_scales + srow + u * kSets * (D / 32));
-        }
+    };
+
+    uint4 kw[kU], vw[kU];
+    uint32_t kc[kU], vc[kU];
+    int32_t next_slot;
+    int64_t next_row;
+    bool more = next_group(next_slot, next_row);
+    if (more) load(p.c.k, p.c.k_scales, next_row, kw, kc);
+    while (more) {
+        const int32_t slot = next_slot;
+        load(p.c.v, p.c.v_scales, next_row, vw, vc);
         float s[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
@@ -106,12 +140,18 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
                 acc = ffma2(q[i], e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), acc);
             s[u] = (acc.x + acc.y) * mx_scale(kc[u]);
         }
+        more = next_group(next_slot, next_row);
+        if (more) load(p.c.k, p.c.k_scales, next_row, kw, kc);
+        // the slots that the row sees
+        uint32_t vis = 0xffffu;
+        if (!(slot >= rv.ws && slot + kGroup - 1 <= min(rv.pos, t.len - 1)))
+            vis = __ballot_sync(0xffffffffu, lane < kGroup && slot + lane < t.end && sees(p, t, rv, h, slot + lane));
         float mx = m;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
 #pragma unroll
             for (int x = 1; x < kLanes; x <<= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
-            if (!kAll) s[u] = (vis >> (u * kSets + set)) & 1u ? s[u] : -INFINITY;
+            s[u] = (vis >> (u * kSets + set)) & 1u ? s[u] : -INFINITY;
             mx = fmaxf(mx, s[u]);
         }
         const float ref = mx == -INFINITY ? 0.f : mx;
@@ -132,42 +172,13 @@ __global__ void __launch_bounds__(kSimtWarps * 32) cache_fwd_simt_kernel(const C
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             // a slot that the row does not see may hold anything (0 * NaN is NaN)
-            if (!kAll && !((vis >> (u * kSets + set)) & 1u)) continue;
+            if (!((vis >> (u * kSets + set)) & 1u)) continue;
             const uint32_t ws[4] = {vw[u].x, vw[u].y, vw[u].z, vw[u].w};
             const float pr = s[u] * mx_scale(vc[u]);
             const float2 pr2 = make_float2(pr, pr);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 o[i] = ffma2(pr2, e4m3x2_to_f32((ws[i / 2] >> (16 * (i % 2))) & 0xffffu), o[i]);
-        }
-    };
-
-    for (int32_t base = g0; base < g1; base += kSimtWarps * 32) {
-        // 32 groups of this warp: which of them the row may see, and their pages
-        const int32_t g = base + lane * kSimtWarps + warp, slot = g * kGroup;
-        bool want = g < g1 && (slot + kGroup > rv.ws || slot + kGroup > t.len);
-        if (g < g1 && !want && p.page_mask) {
-            const int32_t page = slot >> p.c.page_shift;
-            want = (__ldg(p.page_mask + ((int64_t(t.q0) + rv.tok) * p.c.kv_heads + h) * p.mask_words + (page >> 5)) >>
-                    (page & 31)) & 1u;
-        }
-        want = want && (slot <= rv.pos || slot + kGroup > t.len);
-        int32_t id = -1;
-        if (want) {
-            id = cache_page(p.c, t.b, slot >> p.c.page_shift);
-            if (id < 0) cache_range_error(p.c);
-        }
-        uint32_t todo = __ballot_sync(0xffffffffu, id >= 0);
-        while (todo) {
-            const int x = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int32_t s0 = (base + x * kSimtWarps + warp) * kGroup;
-            const int32_t page = __shfl_sync(0xffffffffu, id, x);
-            if (s0 >= rv.ws && s0 + kGroup - 1 <= min(rv.pos, t.len - 1))
-                take(s0, page, std::true_type{}, 0u);
-            else
-                take(s0, page, std::false_type{},
-                     __ballot_sync(0xffffffffu, lane < kGroup && s0 + lane < t.end && sees(p, t, rv, h, s0 + lane)));
         }
     }
 
@@ -276,7 +287,7 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     // longer to set up) where a split still has 1024 slots, none of fewer than 256. (Three rounds,
     // two, one: one event over 16 long histories under four heads 237, 241, 271 us; 16 candidate
     // sets with selected pages 129, 116, 117 us; 8 trees over windows, one round 34, two 43 us.)
-    const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? 7 : plan.tile_rows == 8 ? 4 : 3);
+    const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? simt_blocks(head_dim) : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
     const int64_t items = (work > batch ? work : batch) * kv_heads;
     int64_t n = items > 0 ? (mma ? 2 : 3) * held / items : 1;
