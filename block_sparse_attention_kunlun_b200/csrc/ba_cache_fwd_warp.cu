@@ -16,15 +16,16 @@
 //       pairs them slot by slot; which of the output's rows stands for which column is free
 //       too. P^T comes from S^T by movmatrix.
 // Codes are widened to bf16, exactly (as in ba_cache_fwd_sm100.cu); P is rounded to bf16. Values
-// are on their way while S is formed, the next slots' keys while P V is (a step's loads all at
-// once: 240 us for eight rows and 411 for sixteen, where this takes 233 and 350). Codes that the
-// widening does not know (NaN, scales past 2^7) take part in the MMAs as zeros, and their slots'
-// scores, and their values, are put in in float32: everything else stays the same to the bit.
+// are on their way while S is formed, the next slots' keys while P V is. Slots with codes that the
+// widening does not know (NaN, scales past 2^7) get their scores, and their values, put in in
+// float32 after the MMAs: everything else stays the same to the bit.
 //
-// The case above: 0.97 GB in 233 us, 4.2 TB/s. Bound by the integer pipe and by issue: to
-// put a code's bits into a bf16's places takes three integer operations for two codes, 55% of
-// the integer pipe's time and two thirds of all issue slots, with loads between them. (By the
-// float16 conversion instruction instead: 285 us; with the pages brought into L2 ahead: 267.)
+// The case above: 0.97 GB in 223 us, 4.3 TB/s; with sixteen query heads 313. Bound by the
+// integer pipe and by issue: to put a code's bits into a bf16's places takes four integer
+// operations for two codes, over half of the integer pipe's time and two thirds of all issue
+// slots, with loads between them. (NaN looked for in the codes ahead of the MMAs: 234 and
+// 351; a step's loads all at once: 240 and 411; widened by the float16 conversion instruction:
+// 285; with the pages brought into L2 ahead: 267.)
 #include "ba_cache_fwd.cuh"
 #include "ba_kernels.cuh"
 #include "ba_ptx.cuh"
@@ -51,11 +52,14 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
 }
 
 // Four codes c0 .. c3 as the bf16 pairs (c0, c2) and (c1, c3), each times its half of `factor`:
-// sign, exponent and mantissa moved to a bf16's places are the value times 2^-120.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &even, uint32_t &odd)
+// sign, exponent and mantissa moved to a bf16's places are the value times 2^-120. `top` keeps
+// the largest magnitudes so far, in both halves (see_nan).
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &even, uint32_t &odd, uint32_t &top)
 {
-    const uint32_t x = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-    const uint32_t y = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    const uint32_t mx = (w << 4) & 0x07f007f0u, my = (w >> 4) & 0x07f007f0u;
+    const uint32_t x = mx | ((w << 8) & 0x80008000u);
+    const uint32_t y = my | (w & 0x80008000u);
+    top = __vimax3_u16x2(top, mx, my);
     const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&factor);
     const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), f);
     const __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f);
@@ -65,6 +69,9 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &ev
 
 // 2^(code - 127 + 120) as a bf16 (codes up to 134).
 __device__ __forceinline__ uint32_t bf16_factor(uint32_t code) { return (code << 7) + 0x3c00u; }
+
+// Whether a code widened into `top` was NaN (0x7f0; it was taken for 480).
+__device__ __forceinline__ bool see_nan(uint32_t top) { return ((top + 0x08100810u) & 0x10001000u) != 0; }
 
 // A byte of `nan_bits` has its top bit set when the code there is NaN.
 __device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
@@ -244,44 +251,33 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
         const int64_t row = next_row;
         values.load(v_codes, v_scales, row);
         const bool all = slot >= max_ws && slot <= inside;
-        // codes that the widening does not know. (A scale code over 134: its byte plus 121 carries
-        // into bit 8 of a 16-bit field.)
-        uint32_t odd_keys = 0, odd_values = 0; // slots with such codes
-        {
-            uint32_t odd[2] = {0, 0}, high[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int x = 0; x < KeyCodes<D>::kWords; ++x) odd[i] |= nan_bits(keys.w[i][x]);
-                high[i] = ((keys.scales[i] & 0x00ff00ffu) + 0x00790079u) | (((keys.scales[i] >> 8) & 0x00ff00ffu) + 0x00790079u);
-            }
-            if (__any_sync(0xffffffffu, ((odd[0] | odd[1]) & 0x80808080u) | ((high[0] | high[1]) & 0x01000100u))) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if ((odd[i] & 0x80808080u) | (high[i] & 0x01000100u)) odd_keys |= 1u << (g + 8 * i);
-                odd_keys = __reduce_or_sync(0xffffffffu, odd_keys);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if ((odd_keys >> (g + 8 * i)) & 1u) {
-                        keys.scales[i] = 0;
-#pragma unroll
-                        for (int x = 0; x < KeyCodes<D>::kWords; ++x) keys.w[i][x] = 0;
-                    }
-            }
-        }
         // S^T
         float sc[kTiles][4];
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        uint32_t top[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < KeyCodes<D>::kWords; ++x) {
             // block of the word's columns: (16 t + 64 (x / 4)) / 32
             const int shift = 8 * (t4 / 2 + 2 * (x / 4));
             uint32_t a[4];
-            widen4(keys.w[0][x], bf16_factor((keys.scales[0] >> shift) & 0xffu) * 0x00010001u, a[0], a[2]);
-            widen4(keys.w[1][x], bf16_factor((keys.scales[1] >> shift) & 0xffu) * 0x00010001u, a[1], a[3]);
+            widen4(keys.w[0][x], bf16_factor((keys.scales[0] >> shift) & 0xffu) * 0x00010001u, a[0], a[2], top[0]);
+            widen4(keys.w[1][x], bf16_factor((keys.scales[1] >> shift) & 0xffu) * 0x00010001u, a[1], a[3], top[1]);
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) mma_16x8x16(sc[n], a, q[n][x][0], q[n][x][1]);
+        }
+        // Slots with codes that the widening does not know: their scores, which no other slot's depend
+        // on, are formed again below. (A scale code over 134: its byte plus 121 carries into bit 8 of
+        // a 16-bit field.)
+        uint32_t odd_keys = 0;
+        {
+            bool odd[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                odd[i] = see_nan(top[i]) || ((((keys.scales[i] & 0x00ff00ffu) + 0x00790079u) |
+                                              (((keys.scales[i] >> 8) & 0x00ff00ffu) + 0x00790079u)) & 0x01000100u);
+            if (__any_sync(0xffffffffu, odd[0] || odd[1]))
+                odd_keys = __reduce_or_sync(0xffffffffu, uint32_t(odd[0]) << g | uint32_t(odd[1]) << (g + 8));
         }
         // softmax: values 0, 1 are slot g's for rows 2 t, 2 t + 1, values 2, 3 slot g + 8's
         more = next_group(next_slot, next_row);
@@ -350,28 +346,22 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
             b[n][0] = transpose_8x8(pack_bf16x2(sc[n][0], sc[n][1]));
             b[n][1] = transpose_8x8(pack_bf16x2(sc[n][2], sc[n][3]));
         }
+        // Values under scales that the widening does not know take part as zeros. (NaN codes do as 480,
+        // which a row that does not see them multiplies by 0.)
+        uint32_t odd_values = 0;
         {
-            uint32_t odd = 0, high = 0;
+            uint32_t high = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) high |= values.scale[i] + 0x79u;
+            if (__any_sync(0xffffffffu, high & 0x100u)) {
 #pragma unroll
-                for (int x = 0; x < ValueCodes<D>::kWords; ++x) odd |= nan_bits(values.w[i][x]);
-                high |= values.scale[i] + 0x79u;
-            }
-            if (__any_sync(0xffffffffu, (odd & 0x80808080u) | (high & 0x100u))) {
+                for (int i = 0; i < 4; ++i)
+                    if (values.scale[i] > 134) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool big = values.scale[i] > 134;
-                    odd = 0;
-#pragma unroll
-                    for (int x = 0; x < ValueCodes<D>::kWords; ++x) {
-                        const uint32_t nan = ((nan_bits(values.w[i][x]) & 0x80808080u) >> 7) * 0xffu;
-                        odd |= nan;
-                        values.w[i][x] = big ? 0u : values.w[i][x] & ~nan;
+                        for (int x = 0; x < ValueCodes<D>::kWords; ++x) values.w[i][x] = 0;
+                        values.scale[i] = 0;
+                        odd_values |= 1u << (2 * t4 + (i & 1) + 8 * (i >> 1));
                     }
-                    if (big) values.scale[i] = 0;
-                    if (odd || big) odd_values |= 1u << (2 * t4 + (i & 1) + 8 * (i >> 1));
-                }
                 odd_values = __reduce_or_sync(0xffffffffu, odd_values);
             }
         }
@@ -379,17 +369,29 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
         // the other
         const uint32_t f0 = bf16_factor(values.scale[0]) | bf16_factor(values.scale[1]) << 16;
         const uint32_t f1 = bf16_factor(values.scale[2]) | bf16_factor(values.scale[3]) << 16;
+        top[0] = 0;
 #pragma unroll
         for (int x = 0; x < ValueCodes<D>::kWords; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) { // columns 4 x + 2 y, 4 x + 2 y + 1 of the lane's
                 uint32_t a[4];
-                widen4(__byte_perm(values.w[0][x], values.w[1][x], y ? 0x7632 : 0x5410), f0, a[0], a[1]);
-                widen4(__byte_perm(values.w[2][x], values.w[3][x], y ? 0x7632 : 0x5410), f1, a[2], a[3]);
+                widen4(__byte_perm(values.w[0][x], values.w[1][x], y ? 0x7632 : 0x5410), f0, a[0], a[1], top[0]);
+                widen4(__byte_perm(values.w[2][x], values.w[3][x], y ? 0x7632 : 0x5410), f1, a[2], a[3], top[0]);
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) mma_16x8x16(s.o[n][2 * x + y], a, b[n][0], b[n][1]);
             }
-        // the values that the MMAs took for zeros, for the rows that see them
+        if (__any_sync(0xffffffffu, see_nan(top[0]))) {
+            uint32_t slots = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t nan = 0;
+#pragma unroll
+                for (int x = 0; x < ValueCodes<D>::kWords; ++x) nan |= nan_bits(values.w[i][x]);
+                if (nan & 0x80808080u) slots |= 1u << (2 * t4 + (i & 1) + 8 * (i >> 1));
+            }
+            odd_values |= __reduce_or_sync(0xffffffffu, slots);
+        }
+        // the values that the MMAs did not know, for the rows that see them
         while (odd_values) {
             const int k = __ffs(odd_values) - 1;
             odd_values &= odd_values - 1;
