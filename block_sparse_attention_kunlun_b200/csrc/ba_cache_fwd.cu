@@ -285,8 +285,9 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     // Splits: as many as fill the blocks that 148 SMs hold at once (some more would leave most SMs
     // waiting for the rest), or three times that (twice on the tensor cores, whose blocks take
     // longer to set up) where a split still has 1024 slots, none of fewer than 256. (Three rounds,
-    // two, one: one event over 16 long histories under four heads 237, 241, 271 us; 16 candidate
-    // sets with selected pages 129, 116, 117 us; 8 trees over windows, one round 34, two 43 us.)
+    // two, one: one event over 16 long histories under four heads 223, 233, 264 us, under sixteen
+    // 310, 333, 352, more rounds no less; one row over 8 of them 60 each; 16 candidate sets with
+    // selected pages 130, 118, 116; 8 trees over windows, in splits of fewer slots, 44, 44, 34.)
     const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? simt_blocks(head_dim) : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
     const int64_t items = (work > batch ? work : batch) * kv_heads;
