@@ -644,6 +644,47 @@ def test_rows_behind_the_last_sequence_of_a_padded_batch(rows):
     assert ba.ba_device_status(cache.status) == ba.BA_OK
 
 
+@pytest.mark.parametrize("group,most", [(1, 1), (2, 4), (6, 4), (16, 4)], ids=["one", "eight", "sixteen", "many"])
+def test_many_sequences_some_of_them_empty(group, most):
+    """More sequences than two levels of the blocks' search cover, with and without rows and histories."""
+    batch = 1100
+    rng = np.random.default_rng(group)
+    n = rng.integers(0, most + 1, batch)
+    lens = rng.integers(0, 40, batch) * (rng.random(batch) < 0.8)
+    cache, ref, rng = build(group, lens + n, 1, 64, 16, spare=0)
+    rows, offs = int(n.sum()), offsets(n)
+    q = queries(rng, rows, group, 64)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32(offs), i32(lens), 16, 1)
+    check_attention(got, C.attend(ref, f64(q), offs, lens, 16, 1), 64)
+    mean = torch.from_numpy(rng.normal(size=(ref.k.shape[0], 1, 64))).float()
+    mask = ba.cache_select(cache, q.cuda(), i32(offs), i32(lens), mean.cuda(), 16, 1, 1)
+    assert np.array_equal(mask.cpu().numpy(), C.words(C.select(ref, f64(q), offs, lens, f64(mean), 16, 1, 1)))
+    k, v = ba.cache_read(cache, i32(offs), i32(lens), rows)
+    b, t = np.repeat(np.arange(batch), n), np.concatenate([np.arange(x) for x in n])
+    p = lens[b] + t
+    at = ref.table[b, p // 16], p % 16
+    assert np.array_equal(f64(k)[:, 0], ref.k[at[0], 0, at[1]]) and np.array_equal(f64(v)[:, 0], ref.v[at[0], 0, at[1]])
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
+@pytest.mark.parametrize("rows,pages", [(1, 16384), (9, 16384), (9, 2048)])
+def test_select_of_the_most_pages(rows, pages):
+    table = torch.arange(pages, dtype=torch.int32).flip(0).reshape(1, pages).contiguous().cuda()
+    cache = ba.HistoryCache.empty(pages, 16, 1, 64, table)
+    rng = np.random.default_rng(pages)
+    q = queries(rng, rows, 2, 64)
+    mean = torch.from_numpy(rng.normal(size=(pages, 1, 64))).float()
+    mean[7] = mean[pages - 9]
+    lens = [16 * pages - rows]
+    ref = C.Cache(*(t[:, :, :1].cpu().numpy() for t in (cache.k, cache.v, cache.k_scales, cache.v_scales)), table.cpu())
+    ref.size = 16
+    for topk in (1, 40, pages // 2):
+        got = ba.cache_select(cache, q.cuda(), i32([0, rows]), i32(lens), mean.cuda(), 64, 1, topk)
+        want = C.select(ref, f64(q), [0, rows], lens, f64(mean), 64, 1, topk)
+        assert np.array_equal(got.cpu().numpy(), C.words(want)), topk
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
 def test_nan_in_a_value_column_of_many_rows():
     lens = [100]
     cache, ref, rng = build(4, [140], 1, 128, 16)
