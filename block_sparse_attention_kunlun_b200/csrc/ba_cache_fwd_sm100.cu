@@ -27,13 +27,16 @@
 //
 // 64 trees of 5 to 64 rows over windows of four blocks of 512 (8 heads of 128, 0.25 GB): 124 us;
 // 16 sets of 33 to 64 candidates with 32 selected pages a row (group of two, 0.12 GB): 115 us.
-// Neither bytes nor tensor time bound it (the MMAs are active a quarter of the time), but the
-// chain of a tile: codes, widening, S, softmax, P V, some 3000 cycles, of which the two blocks
-// of an SM overlap half. Without the widening's and the exponentials' arithmetic the first case
-// would take 106 us, without the MMAs too 86; a block's set-up (sequence, Q, page list, TMEM) is
-// 16 of them in the first case and 30 in the second. S in halves of 32 slots, one ahead of the
-// softmax, took 133 us (more and narrower MMAs), codes by loads into registers 179, one block an SM
-// with all roles doubled 270, codes brought into L2 three tiles ahead 130.
+// Not bytes but the chain of a tile bounds it, which the two blocks of an SM overlap by half.
+// Clocked in the first case, in cycles: S's eight MMAs take 340 to issue and 330 more to finish,
+// S's load 260, the maximum 130, the exponentials 710, storing P 135, the hand-over 90, P V's MMAs
+// 410: 2450 at best, 3000 with the other block in the way; widening is a tile ahead. The MMAs take
+// their 750 however few of the 128 rows there are. Without the widening's and the exponentials'
+// arithmetic the first case would take 106 us, without the MMAs too 86; a block's set-up (sequence,
+// Q, page list, TMEM) is 16 of them in the first case and 30 in the second. S in halves of 32
+// slots, one ahead of the softmax, took 133 us (more and narrower MMAs), codes by loads into
+// registers 179, one block an SM with all roles doubled 270, codes brought into L2 three tiles
+// ahead 130.
 //
 // With selected pages the block first lists the units (pages, or halves of 128-slot pages)
 // that any of its rows sees, so that small pages far apart share a tile.
