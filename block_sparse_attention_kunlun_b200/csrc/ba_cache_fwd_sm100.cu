@@ -628,84 +628,93 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&sb.full[st]);
         }
-    } else if (warp == kCopyWarp) {
-        warpgroup_regs_dec<kRegsMma>();
-        // ------------------------------------------------- bulk copies ---
-        // lane 4 x + y copies array y (K, V, their scales) of piece x: a page's slots of this
-        // head, or the half of a 128-slot page that the tile covers
-        const int32_t slots = min(size, kKeys), piece = lane >> 2, array = lane & 3;
-        const bool mine = piece < kKeys / slots;
-        const uint8_t *const src = array == 0 ? p.c.k : array == 1 ? p.c.v : array == 2 ? p.c.k_scales : p.c.v_scales;
-        const uint32_t row_bytes = array < 2 ? D : D / 32;
-        const uint32_t offset = (array == 0 ? 0 : array == 1 ? Lay::kRawV : array == 2 ? Lay::kRawKs : Lay::kRawVs) +
-                                piece * slots * row_bytes;
-        auto slot_of = [&](int32_t i) { return sl.listed ? unit_slot(sl, sb, i, piece) : sl.from + i * kKeys + piece * slots; };
-        auto entry_of = [&](int32_t i) -> int32_t { // page table entry, not checked yet
-            if (!mine || i >= sl.ntiles) return -1;
-            const int32_t us = slot_of(i);
-            return us < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (us >> p.c.page_shift)) : -1;
-        };
-        int32_t next = entry_of(0), i = 0;
-        for (; i < sl.ntiles; ++i) {
-            const int rs = i % Lay::kRawStages;
-            const int32_t id = next;
-            next = entry_of(i + 1);
-            int32_t count = 0; // slots of the piece that there are
-            const int32_t us = slot_of(i);
-            if (uint32_t(id) < uint32_t(p.c.num_pages)) count = min(sl.end - us, slots);
-            else if (mine && us < sl.end) {
-                cache_range_error(p.c);
-                sb.holes = 1;
-            }
-            uint32_t there = 0;
-            if (mine && array == 0)
-                for (int32_t g = 0; g < slots / 16; ++g)
-                    there |= uint32_t(max(0, min(16, count - 16 * g))) << (8 * (piece * (slots / 16) + g));
-            there = __reduce_or_sync(0xffffffffu, there);
-            __syncwarp(); // (holes, before lane 0 arrives)
-            const uint32_t bytes = count > 0 ? slots * row_bytes : 0;
-            const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-            if (!mbar_wait(&sb.raw_empty[rs], ((i / Lay::kRawStages) & 1) ^ 1, abort)) break;
-            if (lane == 0) {
-                sb.there[i % 16] = there;
-                mbar_arrive_expect_tx(&sb.raw_full[rs], total);
-            }
-            __syncwarp();
-            if (bytes)
-                bulk_load(smem + Lay::kRaw0 + rs * Lay::kRawBytes + offset,
-                          src + cache_row(p.c, id, h, us & (size - 1)) * row_bytes, bytes, &sb.raw_full[rs]);
-        }
-        // no copy may be under way when the block ends (after a timed-out wait, too)
-        int late = 0;
-        for (int32_t j = max(0, i - Lay::kRawStages); j < i; ++j)
-            mbar_wait(&sb.raw_full[j % Lay::kRawStages], (j / Lay::kRawStages) & 1, &late);
     } else {
+        // warps 12-15 (one warpgroup: copies, MMA, two idle) hand registers to the softmax
         warpgroup_regs_dec<kRegsMma>();
-        // ---------------------------------------------------- MMA issue ---
-        constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
-        constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-        for (int32_t i = 0; warp == kMmaWarp && i < sl.ntiles; ++i) {
-            const int st = i % S;
-            const uint32_t k_addr = smem_base + 2 * st * Lay::kTileBytes, v_addr = k_addr + Lay::kTileBytes;
-            if (!mbar_wait(&sb.full[st], (i / S) & 1, abort)) break;
-            tc_fence_after();
-            // S over the previous tile's P, whose P V was issued before it
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                mma_ts(tmem + Lay::kColS, tmem + Lay::kColQ + kk * 8,
-                       sdesc_sw128(k_addr + (kk / 4) * Lay::kChunkBytes + (kk % 4) * 32, 16, 1024), idesc_s,
-                       kk > 0 ? 1u : 0u);
-            tc_commit(&sb.s_full);
-            __syncwarp();
-            if (!mbar_wait(&sb.p_full, i & 1, abort)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ts(tmem + Lay::kColO, tmem + Lay::kColS + kk * 8,
-                       sdesc_sw128(v_addr + kk * 2048, Lay::kChunkBytes, 1024), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(&sb.empty[st]);
-            if (i + 1 == sl.ntiles) tc_commit(&sb.o_final);
-            __syncwarp();
+        if (warp == kCopyWarp) {
+            // ------------------------------------------------- bulk copies ---
+            // lane 4 x + y copies array y (K, V, their scales) of piece x: a page's slots of this
+            // head, or the half of a 128-slot page that the tile covers
+            const int32_t slots = min(size, kKeys), piece = lane >> 2, array = lane & 3;
+            const bool mine = piece < kKeys / slots;
+            const uint8_t *const src = array == 0   ? p.c.k
+                                       : array == 1 ? p.c.v
+                                       : array == 2 ? p.c.k_scales
+                                                    : p.c.v_scales;
+            const uint32_t row_bytes = array < 2 ? D : D / 32;
+            const uint32_t offset =
+                (array == 0 ? 0 : array == 1 ? Lay::kRawV : array == 2 ? Lay::kRawKs : Lay::kRawVs) +
+                piece * slots * row_bytes;
+            auto slot_of = [&](int32_t i) {
+                return sl.listed ? unit_slot(sl, sb, i, piece) : sl.from + i * kKeys + piece * slots;
+            };
+            auto entry_of = [&](int32_t i) -> int32_t { // page table entry, not checked yet
+                if (!mine || i >= sl.ntiles) return -1;
+                const int32_t us = slot_of(i);
+                return us < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (us >> p.c.page_shift)) : -1;
+            };
+            int32_t next = entry_of(0), i = 0;
+            for (; i < sl.ntiles; ++i) {
+                const int rs = i % Lay::kRawStages;
+                const int32_t id = next;
+                next = entry_of(i + 1);
+                int32_t count = 0; // slots of the piece that there are
+                const int32_t us = slot_of(i);
+                if (uint32_t(id) < uint32_t(p.c.num_pages)) count = min(sl.end - us, slots);
+                else if (mine && us < sl.end) {
+                    cache_range_error(p.c);
+                    sb.holes = 1;
+                }
+                uint32_t there = 0;
+                if (mine && array == 0)
+                    for (int32_t g = 0; g < slots / 16; ++g)
+                        there |= uint32_t(max(0, min(16, count - 16 * g))) << (8 * (piece * (slots / 16) + g));
+                there = __reduce_or_sync(0xffffffffu, there);
+                __syncwarp(); // (holes, before lane 0 arrives)
+                const uint32_t bytes = count > 0 ? slots * row_bytes : 0;
+                const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+                if (!mbar_wait(&sb.raw_empty[rs], ((i / Lay::kRawStages) & 1) ^ 1, abort)) break;
+                if (lane == 0) {
+                    sb.there[i % 16] = there;
+                    mbar_arrive_expect_tx(&sb.raw_full[rs], total);
+                }
+                __syncwarp();
+                if (bytes)
+                    bulk_load(smem + Lay::kRaw0 + rs * Lay::kRawBytes + offset,
+                              src + cache_row(p.c, id, h, us & (size - 1)) * row_bytes, bytes, &sb.raw_full[rs]);
+            }
+            // no copy may be under way when the block ends (after a timed-out wait, too)
+            int late = 0;
+            for (int32_t j = max(0, i - Lay::kRawStages); j < i; ++j)
+                mbar_wait(&sb.raw_full[j % Lay::kRawStages], (j / Lay::kRawStages) & 1, &late);
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------- MMA issue ---
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+            for (int32_t i = 0; i < sl.ntiles; ++i) {
+                const int st = i % S;
+                const uint32_t k_addr = smem_base + 2 * st * Lay::kTileBytes, v_addr = k_addr + Lay::kTileBytes;
+                if (!mbar_wait(&sb.full[st], (i / S) & 1, abort)) break;
+                tc_fence_after();
+                // S over the previous tile's P, whose P V was issued before it
+    #pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ts(tmem + Lay::kColS, tmem + Lay::kColQ + kk * 8,
+                           sdesc_sw128(k_addr + (kk / 4) * Lay::kChunkBytes + (kk % 4) * 32, 16, 1024), idesc_s,
+                           kk > 0 ? 1u : 0u);
+                tc_commit(&sb.s_full);
+                __syncwarp();
+                if (!mbar_wait(&sb.p_full, i & 1, abort)) break;
+                tc_fence_after();
+    #pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                    mma_ts(tmem + Lay::kColO, tmem + Lay::kColS + kk * 8,
+                           sdesc_sw128(v_addr + kk * 2048, Lay::kChunkBytes, 1024), idesc_o,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(&sb.empty[st]);
+                if (i + 1 == sl.ntiles) tc_commit(&sb.o_final);
+                __syncwarp();
+            }
         }
     }
 
