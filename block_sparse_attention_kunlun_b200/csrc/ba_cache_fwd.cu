@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D)) cache_fwd_sim
                                        __uint_as_float(ws[x] & 0xffff0000u) * p.scale_log2);
     }
     // this split's slots, in groups of 16
-    const int32_t lo = (p.page_mask ? 0 : rv.ws) / kGroup * kGroup;
+    const int32_t lo = first_slot(p, t, rv.ws) / kGroup * kGroup;
     int64_t from = lo + int64_t(split) * p.chunk, to = split + 1 == p.nsplit ? t.end : from + p.chunk;
     if (to > t.end) to = t.end;
     // `from` is a multiple of 16; a split that starts past the end has nothing

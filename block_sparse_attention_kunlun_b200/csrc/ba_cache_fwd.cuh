@@ -59,6 +59,14 @@ __device__ __forceinline__ RowView row_view(const CacheFwd &p, const FwdTile &t,
     return r;
 }
 
+// First slot that rows whose windows start at `ws` or later may see: any page may be selected, and the
+// rows' own slots come after the cached ones even where their positions (and windows) lie past the
+// cache's last slot.
+__device__ __forceinline__ int32_t first_slot(const CacheFwd &p, const FwdTile &t, int32_t ws)
+{
+    return p.page_mask ? 0 : min(ws, t.len);
+}
+
 // Whether row r sees slot s (s < t.end).
 __device__ __forceinline__ bool sees(const CacheFwd &p, const FwdTile &t, const RowView &r, int32_t h, int32_t s)
 {

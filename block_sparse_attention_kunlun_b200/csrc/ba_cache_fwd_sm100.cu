@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     if (!p.tree && !p.q.positions)
         sl.end = int32_t(min(int64_t(t.end), int64_t(t.len) + (t.row0 + t.rows - 1) / p.q.group + 1));
     const int32_t min_ws = sb.min_ws;
-    const int64_t from = (sl.listed ? 0 : min_ws / kKeys * kKeys) + int64_t(split) * p.chunk;
+    const int64_t from = first_slot(p, t, min_ws) / kKeys * kKeys + int64_t(split) * p.chunk;
     int64_t to = split + 1 == p.nsplit ? sl.end : from + p.chunk;
     if (to > sl.end) to = sl.end;
     sl.from = int32_t(min(from, int64_t(sl.end)));

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kWarpCount * 32, kN == 8 ? 4 : 3)
     }
 
     // this split's slots, in groups of 16
-    const int32_t lo = (p.page_mask ? 0 : min_ws) / kGroup * kGroup;
+    const int32_t lo = first_slot(p, t, min_ws) / kGroup * kGroup;
     int64_t from = lo + int64_t(split) * p.chunk, to = split + 1 == p.nsplit ? t.end : from + p.chunk;
     if (to > t.end) to = t.end;
     // `from` is a multiple of 16; a split that starts past the end has nothing
