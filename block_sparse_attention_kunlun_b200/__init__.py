@@ -577,9 +577,34 @@ def _check_inputs(q, k, v, seq_offsets):
         raise ValueError("seq_offsets must be an int32 CUDA tensor")
 
 
-def workspace_for(nbytes: int, device) -> torch.Tensor:
+def _launch_stream(stream, device):
+    """The stream argument of a call as torch's stream on `device`."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    raw = _stream(stream)
+    # (0 and 1 are both CUDA's default stream)
+    return torch.cuda.ExternalStream(raw, device=device) if raw > 1 else torch.cuda.default_stream(device)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """An uninitialised tensor for a call that launches on `stream` (None: the current one). Torch reuses a
+    freed block in the order of the stream it was allocated on, so it is allocated on the call's; a tensor that
+    is returned stays out of reuse until the work of the caller's stream at its end is done, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    launch = _launch_stream(stream, device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(launch):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and launch != caller:
+        t.record_stream(caller)
+    return t
+
+
+def workspace_for(nbytes: int, device, stream=None) -> torch.Tensor:
+    """A workspace for calls on `stream` (None: the current one)."""
     # torch's caching allocator returns 512-byte-aligned blocks
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return _empty(max(int(nbytes), 256), torch.uint8, device, stream, returned=False)
 
 
 def block_attention_fwd(q, k, v, seq_offsets, block, window, skip=None, out=None, lse=None,
@@ -860,7 +885,7 @@ def cache_read(cache, row_offsets, starts, total_rows, dtype=torch.bfloat16, k=N
     if (k is None) != (v is None):
         raise ValueError("pass both k and v, or neither")
     if k is None:
-        k, v = (torch.empty((total_rows, *cache._row), dtype=dtype, device=cache.device) for _ in "kv")
+        k, v = (_empty((total_rows, *cache._row), dtype, cache.device, stream) for _ in "kv")
     _check_rows(cache, k, v, row_offsets, starts)
     if k.shape[0] != total_rows:
         raise ValueError(f"k and v must have {total_rows} rows")
@@ -910,7 +935,7 @@ def cache_select(cache, q, q_offsets, lens, summaries, block, window, topk, posi
     kv_heads = cache._row[0]
     words, means = (prob.total_tokens, kv_heads, cache._words), (cache.struct.num_pages, *cache._row)
     if page_mask is None:
-        page_mask = torch.empty(words, dtype=torch.int32, device=cache.device)
+        page_mask = _empty(words, torch.int32, cache.device, stream)
     if not (_fits(cache, summaries, torch.float32, means) and _fits(cache, page_mask, torch.int32, words)):
         _refuse(cache, (("summaries", summaries, torch.float32, means), ("page_mask", page_mask, torch.int32, words)))
     st = _load().ba_cache_select(cache._ref, ctypes.byref(prob), q.data_ptr(), q_offsets.data_ptr(), lens.data_ptr(),
@@ -931,9 +956,9 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
     prob = _check_queries(cache, q, q_offsets, lens, positions)
     rows, heads = prob.total_tokens, prob.heads
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, torch.bfloat16, cache.device, stream)
     if lse is None:
-        lse = torch.empty((heads, rows), dtype=torch.float32, device=q.device)
+        lse = _empty((heads, rows), torch.float32, cache.device, stream)
     named = [("out", out, torch.bfloat16, q.shape), ("lse", lse, torch.float32, (heads, rows))]
     words = 0
     if tree_mask is not None:
@@ -950,7 +975,8 @@ def cache_attention_fwd(cache, q, q_offsets, lens, block, window, positions=None
             _refuse(cache, named)
     ref = ctypes.byref(prob)
     if workspace is None:
-        workspace = workspace_for(_load().ba_cache_fwd_workspace_size(cache._ref, ref, block, window), q.device)
+        need = _load().ba_cache_fwd_workspace_size(cache._ref, ref, block, window)
+        workspace = workspace_for(need, cache.device, stream)
     elif workspace.get_device() != cache._index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
     st = _load().ba_cache_fwd(cache._ref, ref, q.data_ptr(), q_offsets.data_ptr(), lens.data_ptr(), _ptr(positions),

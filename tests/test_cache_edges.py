@@ -40,3 +40,61 @@ def test_positions_past_the_cached_slots(rows, D, selected):
     assert np.isfinite(want[1]).all()
     check(got, want, D)
     assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
+def busy_block(like):
+    """Leaves a freed block of `like`'s size whose last write, on the current stream, is still to come."""
+    x = torch.empty_like(like)
+    torch.cuda._sleep(50_000_000)
+    x.view(torch.uint8).fill_(0x7F)
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_results_on_an_explicit_stream_do_not_lie_in_busy_memory(as_number):
+    """Results that the binding allocates for a call on another stream must not be a block that work of the
+    current stream has still to write (the allocator hands freed blocks out at once)."""
+    cache, ref, rng = build(5, [3000, 2500], 2, 128, 16)
+    offs, lens = i32([0, 1, 2]), i32([2900, 2400])
+    q = queries(rng, 2, 4, 128).cuda()
+    mean = torch.from_numpy(rng.normal(size=(ref.k.shape[0], 2, 128))).float().cuda()
+    calls = {
+        "attention": lambda **kw: ba.cache_attention_fwd(cache, q, offs, lens, 1 << 20, 1, **kw),
+        "read": lambda **kw: ba.cache_read(cache, offs, lens, 2, **kw),
+        "select": lambda **kw: (ba.cache_select(cache, q, offs, lens, mean, 64, 1, 4, **kw),),
+    }
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        for t in want:
+            busy_block(t)
+        got = call(stream=side.cuda_stream if as_number else side)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), name
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_calls_on_explicit_streams_share_no_workspace(rows):
+    """Split attention on two explicit streams at once, workspaces from the binding, while the current stream
+    fills freed blocks of the workspace's size: every result equals the call alone."""
+    cache, _, rng = build(21, [5000, 4000], 2, 128, 64)
+    args = []
+    for lens in ([4900, 3900], [4800, 3950]):
+        q = queries(rng, 2 * rows, 2, 128).cuda()
+        args.append((q, i32([0, rows, 2 * rows]), i32(lens), 1 << 20, 1))
+    need = ba.ba_cache_fwd_workspace_size(cache, ba.make_problem(args[0][0], args[0][1]), 1 << 20, 1)
+    assert need > 0
+    want = [ba.cache_attention_fwd(cache, *a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    outs = [[(torch.empty_like(a[0]), torch.empty((2, 2 * rows), device="cuda")) for _ in range(40)] for a in args]
+    torch.cuda.synchronize()
+    for i in range(40):
+        for s, a, o in zip(streams, args, outs):
+            ba.cache_attention_fwd(cache, *a, out=o[i][0], lse=o[i][1], stream=s)
+        for _ in range(3):
+            ba.workspace_for(need, "cuda").fill_(0x7F)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for out, lse in o:
+            assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
