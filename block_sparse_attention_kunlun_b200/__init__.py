@@ -303,9 +303,9 @@ def gdpa_fwd(q, k, v, seq_offsets, block, window, activation="gelu", out=None, w
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if workspace is None:
-        workspace = workspace_for(ba_gdpa_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_gdpa_workspace_size(prob, block, window), q.device, stream)
     st = ba_gdpa_fwd(prob, activation, q, k, v, seq_offsets, block, window, out, workspace, stream=stream)
     if st != BA_OK:
         raise BAError(st, "ba_gdpa_fwd")
@@ -317,11 +317,11 @@ def gdpa_bwd(q, k, v, dout, seq_offsets, block, window, activation="gelu", dq=No
     """Gradients of gdpa_fwd: allocates dq/dk/dv (and a workspace) with torch and runs ba_gdpa_bwd."""
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(q.shape, q.dtype, q.device, stream) if dv is None else dv
     if workspace is None:
-        workspace = workspace_for(ba_gdpa_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_gdpa_workspace_size(prob, block, window), q.device, stream)
     st = ba_gdpa_bwd(prob, activation, q, k, v, dout, seq_offsets, block, window, dq, dk, dv, workspace,
                      stream=stream)
     if st != BA_OK:
@@ -374,9 +374,9 @@ def gdpa_cross_fwd(q, k, v, q_offsets, kv_offsets, activation="gelu", out=None, 
     _check_cross(q, k, v, q_offsets, kv_offsets)
     prob = make_problem(q, q_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if workspace is None:
-        workspace = workspace_for(ba_gdpa_cross_workspace_size(prob, k.shape[0]), q.device)
+        workspace = workspace_for(ba_gdpa_cross_workspace_size(prob, k.shape[0]), q.device, stream)
     st = ba_gdpa_cross_fwd(prob, k.shape[0], activation, q, k, v, q_offsets, kv_offsets, out, workspace,
                            stream=stream)
     if st != BA_OK:
@@ -389,11 +389,11 @@ def gdpa_cross_bwd(q, k, v, dout, q_offsets, kv_offsets, activation="gelu", dq=N
     """Gradients of gdpa_cross_fwd (ba_gdpa_cross_bwd)."""
     _check_cross(q, k, v, q_offsets, kv_offsets)
     prob = make_problem(q, q_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
     if workspace is None:
-        workspace = workspace_for(ba_gdpa_cross_workspace_size(prob, k.shape[0]), q.device)
+        workspace = workspace_for(ba_gdpa_cross_workspace_size(prob, k.shape[0]), q.device, stream)
     st = ba_gdpa_cross_bwd(prob, k.shape[0], activation, q, k, v, dout, q_offsets, kv_offsets, dq, dk, dv,
                            workspace, stream=stream)
     if st != BA_OK:
@@ -413,8 +413,9 @@ def mx_quantize(x, stream=None):
     (elements uint8 [rows, heads, head_dim] holding E4M3 codes, scales uint8
     [rows, heads rounded up to 4, head_dim / 32] holding E8M0 codes)."""
     rows, heads, head_dim = x.shape
-    elements = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    scales = torch.zeros((rows, (heads + 3) // 4 * 4, head_dim // 32), dtype=torch.uint8, device=x.device)
+    elements = _empty(x.shape, torch.uint8, x.device, stream)
+    shape = (rows, (heads + 3) // 4 * 4, head_dim // 32)
+    scales = _empty(shape, torch.uint8, x.device, stream, make=torch.zeros)
     st = ba_mx_quantize(x, elements, scales, stream)
     if st != BA_OK:
         raise BAError(st, "ba_mx_quantize")
@@ -442,11 +443,11 @@ def mx_block_attention_fwd(q, k, v, seq_offsets, block, window, skip=None, out=N
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = _empty((q.shape[1], q.shape[0]), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = workspace_for(ba_mx_fwd_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_mx_fwd_workspace_size(prob, block, window), q.device, stream)
     st = ba_mx_fwd(prob, q, k, v, seq_offsets, block, window, skip, out, lse, workspace, stream=stream)
     if st != BA_OK:
         raise BAError(st, "ba_mx_fwd")
@@ -474,11 +475,11 @@ def mx_block_attention_bwd(q, k, v, out, lse, dout, seq_offsets, block, window, 
     (and a workspace) with torch."""
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(q.shape, q.dtype, q.device, stream) if dv is None else dv
     if workspace is None:
-        workspace = workspace_for(ba_mx_bwd_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_mx_bwd_workspace_size(prob, block, window), q.device, stream)
     st = ba_mx_bwd(prob, q, k, v, out, lse, dout, seq_offsets, block, window, skip, dq, dk, dv, workspace,
                    stream=stream)
     if st != BA_OK:
@@ -586,16 +587,16 @@ def _launch_stream(stream, device):
     return torch.cuda.ExternalStream(raw, device=device) if raw > 1 else torch.cuda.default_stream(device)
 
 
-def _empty(shape, dtype, device, stream, returned=True):
-    """An uninitialised tensor for a call that launches on `stream` (None: the current one). Torch reuses a
+def _empty(shape, dtype, device, stream, returned=True, make=torch.empty):
+    """An uninitialised (or make's) tensor for a call that launches on `stream` (None: the current one). Torch reuses a
     freed block in the order of the stream it was allocated on, so it is allocated on the call's; a tensor that
     is returned stays out of reuse until the work of the caller's stream at its end is done, too."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     launch = _launch_stream(stream, device)
     caller = torch.cuda.current_stream(device)
     with torch.cuda.stream(launch):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make(shape, dtype=dtype, device=device)
     if returned and launch != caller:
         t.record_stream(caller)
     return t
@@ -613,11 +614,11 @@ def block_attention_fwd(q, k, v, seq_offsets, block, window, skip=None, out=None
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = _empty((q.shape[1], q.shape[0]), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = workspace_for(ba_fwd_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_fwd_workspace_size(prob, block, window), q.device, stream)
     st = ba_fwd(prob, q, k, v, seq_offsets, block, window, skip, out, lse, workspace, stream=stream)
     if st != BA_OK:
         raise BAError(st, "ba_fwd")
@@ -629,11 +630,11 @@ def block_attention_bwd(q, k, v, out, lse, dout, seq_offsets, block, window, ski
     """Allocates dq/dk/dv (and a workspace) with torch and runs ba_bwd."""
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(q.shape, q.dtype, q.device, stream) if dv is None else dv
     if workspace is None:
-        workspace = workspace_for(ba_bwd_workspace_size(prob, block, window), q.device)
+        workspace = workspace_for(ba_bwd_workspace_size(prob, block, window), q.device, stream)
     st = ba_bwd(prob, q, k, v, out, lse, dout, seq_offsets, block, window, skip, dq, dk, dv,
                 workspace, stream=stream)
     if st != BA_OK:
@@ -648,11 +649,11 @@ def sliding_window_attention_fwd(q, k, v, seq_offsets, window_tokens, skip=None,
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = _empty((q.shape[1], q.shape[0]), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = workspace_for(ba_swa_fwd_workspace_size(prob, window_tokens), q.device)
+        workspace = workspace_for(ba_swa_fwd_workspace_size(prob, window_tokens), q.device, stream)
     st = ba_swa_fwd(prob, q, k, v, seq_offsets, window_tokens, skip, out, lse, workspace, stream=stream)
     if st != BA_OK:
         raise BAError(st, "ba_swa_fwd")
@@ -664,11 +665,11 @@ def sliding_window_attention_bwd(q, k, v, out, lse, dout, seq_offsets, window_to
     """Allocates dq/dk/dv (and a workspace) with torch and runs ba_swa_bwd."""
     _check_inputs(q, k, v, seq_offsets)
     prob = make_problem(q, seq_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(q.shape, q.dtype, q.device, stream) if dv is None else dv
     if workspace is None:
-        workspace = workspace_for(ba_swa_bwd_workspace_size(prob, window_tokens), q.device)
+        workspace = workspace_for(ba_swa_bwd_workspace_size(prob, window_tokens), q.device, stream)
     st = ba_swa_bwd(prob, q, k, v, out, lse, dout, seq_offsets, window_tokens, skip, dq, dk, dv,
                     workspace, stream=stream)
     if st != BA_OK:
@@ -703,12 +704,12 @@ def rope_block_attention_fwd(q, k, v, seq_offsets, block, window, cos, sin, skip
     _check_rotated(q_rot, k_rot, q)
     prob = make_problem(q, seq_offsets)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        lse = _empty((q.shape[1], q.shape[0]), torch.float32, q.device, stream)
     if workspace is None:
         need = (ba_fwd_workspace_size if q_rot is not None else ba_rope_fwd_workspace_size)(prob, block, window)
-        workspace = workspace_for(need, q.device)
+        workspace = workspace_for(need, q.device, stream)
     st = ba_rope_fwd(prob, make_rope(cos, sin, q_rot, k_rot), q, k, v, seq_offsets, block, window, skip, out,
                      lse, workspace, stream=stream)
     if st != BA_OK:
@@ -725,12 +726,12 @@ def rope_block_attention_bwd(q, k, v, out, lse, dout, seq_offsets, block, window
     _check_tables(cos, sin, q)
     _check_rotated(q_rot, k_rot, q)
     prob = make_problem(q, seq_offsets)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(q.shape, q.dtype, q.device, stream) if dv is None else dv
     if workspace is None:
         need = (ba_bwd_workspace_size if q_rot is not None else ba_rope_bwd_workspace_size)(prob, block, window)
-        workspace = workspace_for(need, q.device)
+        workspace = workspace_for(need, q.device, stream)
     st = ba_rope_bwd(prob, make_rope(cos, sin, q_rot, k_rot), q, k, v, out, lse, dout, seq_offsets, block,
                      window, skip, dq, dk, dv, workspace, stream=stream)
     if st != BA_OK:
