@@ -796,9 +796,12 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
                           uint32_t *page_mask, cudaStream_t stream)
 {
     auto kern = cache_select_kernel<D, kRows>;
-    const size_t smem = size_t(kRows) * c.max_pages * 8;
+    const size_t smem = size_t(kRows) * c.max_pages * 8; // (eight rows: max_pages <= kSelectMaxPages / 8)
     if (smem > 43 * 1024) { // (beside up to 5 KB of static shared memory)
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        // the most that any call needs: a limit of this call's own would be taken from one that another
+        // thread is about to launch
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSelectMaxPages) * 8);
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(kRows > 1 ? q.rows / kRows + c.batch : q.rows, c.kv_heads);

@@ -1,5 +1,8 @@
 """GPU tests of the history cache where its calls meet less usual arguments: positions past the cache's slots,
 splits with selected pages, padded batches. Bounds are test_cache.py's; a NaN fails them here."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -98,3 +101,36 @@ def test_calls_on_explicit_streams_share_no_workspace(rows):
     for o, w in zip(outs, want):
         for out, lse in o:
             assert torch.equal(out, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+def test_threads_select_over_caches_of_different_sizes(rows):
+    """Host threads, each with its own stream and cache: a call's shared memory is its own affair."""
+    work = []
+    for i in range(8):
+        pages = (16384, 7000)[i % 2] if rows == 1 else (2048, 900)[i % 2]
+        table = torch.arange(pages, dtype=torch.int32).reshape(1, pages).cuda()
+        cache = ba.HistoryCache.empty(pages, 16, 1, 64, table)
+        rng = np.random.default_rng(i)
+        mean = torch.from_numpy(rng.normal(size=(pages, 1, 64))).float().cuda()
+        q, offs, lens = queries(rng, rows, 1, 64).cuda(), i32([0, rows]), i32([1000])
+        want = ba.cache_select(cache, q, offs, lens, mean, 64, 1, 3)
+        mask, stream = torch.zeros_like(want), torch.cuda.Stream()
+        args = (ctypes.byref(cache.struct), ctypes.byref(ba.make_problem(q, offs)), q.data_ptr(), offs.data_ptr(),
+                lens.data_ptr(), None, mean.data_ptr(), 64, 1, 3, mask.data_ptr(), stream.cuda_stream)
+        work.append((args, mask, want, (cache, q, offs, lens, mean, stream)))
+    select, codes = ba._load().ba_cache_select, []
+
+    def serve(args):
+        codes.append({select(*args) for _ in range(5000)})
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=serve, args=(w[0],)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{ba.BA_OK}] * len(work)
+    for _, mask, want, _ in work:
+        assert torch.equal(mask, want)
