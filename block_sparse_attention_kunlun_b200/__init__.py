@@ -748,7 +748,9 @@ class HistoryCache:
     k_scales, v_scales: uint8 [num_pages, kv_heads, page_size, head_dim / 32]
     (E8M0 codes); page_table: int32 [batch, max_pages]; status: int32 CUDA
     tensor of one word, zeroed here when not given. The tensors are kept, not
-    copied: the caller changes page_table in place as histories grow.
+    copied, and the calls read their addresses as they were: the caller changes
+    page_table in place as histories grow, and makes another HistoryCache on the
+    same pools for a wider one (attributes cannot be assigned to).
     """
 
     __slots__ = ("k", "v", "k_scales", "v_scales", "page_table", "status", "struct", "batch", "device", "_ref",
@@ -773,14 +775,24 @@ class HistoryCache:
                         ("page_table", page_table), ("status", status)):
             if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
                 raise ValueError(f"{name} must be a contiguous CUDA tensor on k's device")
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.page_table, self.status = page_table, status
-        self.batch, self.device = page_table.shape[0], k.device
-        self.struct = BACache(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                              page_table.data_ptr(), status.data_ptr(), page_table.shape[0], page_table.shape[1],
-                              num_pages, page_size, kv_heads, head_dim)
-        self._ref, self._index = ctypes.byref(self.struct), k.get_device()
-        self._row, self._words = (kv_heads, head_dim), (page_table.shape[1] + 31) // 32
+        struct = BACache(k.data_ptr(), v.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                         page_table.data_ptr(), status.data_ptr(), page_table.shape[0], page_table.shape[1],
+                         num_pages, page_size, kv_heads, head_dim)
+        for name, x in (("k", k), ("v", v), ("k_scales", k_scales), ("v_scales", v_scales),
+                        ("page_table", page_table), ("status", status), ("struct", struct),
+                        ("batch", page_table.shape[0]), ("device", k.device), ("_ref", ctypes.byref(struct)),
+                        ("_index", k.get_device()), ("_row", (kv_heads, head_dim)),
+                        ("_words", (page_table.shape[1] + 31) // 32)):
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} is the cache's for good: change its contents, or make another HistoryCache")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
+
+    def __reduce__(self):
+        return HistoryCache, (self.k, self.v, self.k_scales, self.v_scales, self.page_table, self.status)
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, page_table):

@@ -1,5 +1,6 @@
 """GPU tests of the history cache where its calls meet less usual arguments: positions past the cache's slots,
 splits with selected pages, padded batches. Bounds are test_cache.py's; a NaN fails them here."""
+import copy
 import ctypes
 import threading
 
@@ -134,3 +135,20 @@ def test_threads_select_over_caches_of_different_sizes(rows):
     assert codes == [{ba.BA_OK}] * len(work)
     for _, mask, want, _ in work:
         assert torch.equal(mask, want)
+
+
+def test_a_cache_keeps_its_tensors():
+    """The calls read the tensors' addresses as they were when the cache was made: none can be put in another's
+    place. A wider page table is another cache on the same pools; a copy has tensors of its own."""
+    cache, ref, rng = build(2, [40], 1, 64, 16)
+    with pytest.raises(AttributeError):
+        cache.page_table = torch.zeros((1, 9), dtype=torch.int32, device="cuda")
+    wide = torch.full((1, 40), -1, dtype=torch.int32, device="cuda")
+    wide[:, :cache.page_table.shape[1]] = cache.page_table
+    wider = ba.HistoryCache(cache.k, cache.v, cache.k_scales, cache.v_scales, wide, status=cache.status)
+    twin = copy.deepcopy(cache)
+    assert twin.k.data_ptr() != cache.k.data_ptr() and twin.struct.k == twin.k.data_ptr()
+    for c in (wider, twin):
+        k, v = ba.cache_read(c, i32([0, 40]), i32([0]), 40)
+        pages, at = ref.table[0, np.arange(40) // 16], np.arange(40) % 16
+        assert np.array_equal(f64(k)[:, 0], ref.k[pages, 0, at]) and np.array_equal(f64(v)[:, 0], ref.v[pages, 0, at])
