@@ -272,14 +272,17 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
 {
     CacheFwdPlan plan;
     const int64_t all = int64_t(rows) * group; // query rows of a key/value head
-    const int64_t each = batch > 0 ? (all + batch - 1) / batch : 1;
+    // sequences that can have rows: a batch padded with empty ones is planned as the rest of it, and no
+    // sequence counts for less than the rows that one token brings
+    const int64_t live = batch < rows ? batch : rows;
+    const int64_t each = live > 0 ? (all + live - 1) / live : 1;
     plan.tile_rows = each <= 1 ? 1 : (each <= 8 ? 8 : (each <= 16 ? 16 : kMmaRows));
     const bool mma = plan.tile_rows == kMmaRows;
     plan.tiles = plan.tile_rows > 1 ? all / plan.tile_rows + batch : all;
     // the most slots a tile may meet: the whole cache, or the window and the rows themselves
     int64_t reach = slots;
     if (!has_mask) {
-        const int64_t per = batch > 0 ? (int64_t(rows) + batch - 1) / batch : 0;
+        const int64_t per = live > 0 ? (int64_t(rows) + live - 1) / live : 0;
         if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
     }
     // Splits: as many as fill the blocks that 148 SMs hold at once (some more would leave most SMs
@@ -290,7 +293,7 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     // selected pages 130, 118, 116; 8 trees over windows, in splits of fewer slots, 44, 44, 34.)
     const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? simt_blocks(head_dim) : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
-    const int64_t items = (work > batch ? work : batch) * kv_heads;
+    const int64_t items = (work > live ? work : live) * kv_heads;
     int64_t n = items > 0 ? (mma ? 2 : 3) * held / items : 1;
     if (n > 1 && reach / n < 1024) n = held / items;
     const int64_t most = (reach + 255) / 256;

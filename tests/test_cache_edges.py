@@ -152,3 +152,23 @@ def test_a_cache_keeps_its_tensors():
         k, v = ba.cache_read(c, i32([0, 40]), i32([0]), 40)
         pages, at = ref.table[0, np.arange(40) // 16], np.arange(40) % 16
         assert np.array_equal(f64(k)[:, 0], ref.k[pages, 0, at]) and np.array_equal(f64(v)[:, 0], ref.v[pages, 0, at])
+
+
+@pytest.mark.parametrize("group", [1, 4, 16, 20])
+@pytest.mark.parametrize("slots", [200, 6000])
+def test_empty_sequences_change_nothing(slots, group):
+    """Single events of four sequences, alone and in a batch padded with sixty empty ones: the same kernel in the
+    same splits, bit for bit."""
+    lens = [slots, slots - 70, 3, slots // 2]
+    cache, ref, rng = build(slots + group, [n + 1 for n in lens], 2, 64, 16)
+    q = queries(rng, 4, 2 * group, 64)
+    alone = ba.cache_attention_fwd(cache, q.cuda(), i32([0, 1, 2, 3, 4]), i32(lens), 1 << 20, 1)
+    check(alone, C.attend(ref, f64(q), [0, 1, 2, 3, 4], lens, 1 << 20, 1), 64)
+    at = [5, 6, 40, 63]
+    n, padded = np.zeros(64, dtype=int), np.zeros(64, dtype=int)
+    n[at], padded[at] = 1, lens
+    table = torch.full((64, cache.page_table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    table[at] = cache.page_table
+    wide = ba.HistoryCache(cache.k, cache.v, cache.k_scales, cache.v_scales, table)
+    got = ba.cache_attention_fwd(wide, q.cuda(), i32(offsets(n)), i32(padded), 1 << 20, 1)
+    assert torch.equal(got[0], alone[0]) and torch.equal(got[1], alone[1])
