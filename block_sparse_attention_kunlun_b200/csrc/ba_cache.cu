@@ -814,9 +814,12 @@ cudaError_t launch_select(const CacheView &c, const CacheQuery &q, const float *
 cudaError_t launch_cache_select(const CacheView &c, const CacheQuery &q, const float *summaries, int32_t topk,
                                 uint32_t *page_mask, cudaStream_t stream)
 {
-    // eight rows a block read each mean once; single events, and rows whose eight key arrays
-    // would not fit in shared memory, go one row a block
-    const bool eight = int64_t(q.rows) > 2 * int64_t(c.batch) && c.max_pages <= kSelectMaxPages / 8;
+    // Eight rows a block read each mean once; single events go one row a block. (us, 8 heads of 128,
+    // one row a block and eight: 64 histories of 64 full pages, one event 9.4 and 12.8, two rows 13.9 and
+    // 13.1, four 22.7 and 13.5; of 512 pages 37 and 45, 56 and 47, 100 and 51; 8 histories of 2000 pages
+    // 65 and 53, 68 and 57, 72 and 56.) Rows whose eight key arrays would not fit in shared memory have to
+    // go one by one, and read each mean again: 8 trees of 40 rows over 2047 pages 175, over 2065 407.
+    const bool eight = q.rows > c.batch && c.max_pages <= kSelectMaxPages / 8;
     if (c.head_dim == 64)
         return eight ? launch_select<64, 8>(c, q, summaries, topk, page_mask, stream)
                      : launch_select<64, 1>(c, q, summaries, topk, page_mask, stream);

@@ -226,3 +226,16 @@ def test_a_padded_batch_has_the_same_results(rows):
         ba.cache_attention_fwd(cache, q.cuda(), i32([0, rows]), i32(lens), block, 1, out=out, lse=lse)
         assert torch.isnan(out[rows:]).all() and torch.isnan(lse[:, rows:]).all()
         check((out[:rows], lse[:, :rows]), C.attend(ref, f64(q[:rows]), [0, rows], lens, block, 1), 64)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1, 1], [2, 1, 1, 1], [2, 2, 2, 2], [0, 0, 4, 0], [0, 5, 0, 0]])
+@pytest.mark.parametrize("group", [1, 3])
+def test_select_of_one_and_two_rows_a_sequence(n, group):
+    """Around the border between the kernel for single events and the one for eight rows."""
+    lens = [900, 16, 700, 333]
+    cache, ref, rng = build(sum(n) + group, [a + b for a, b in zip(lens, n)], 2, 128, 16)
+    q = queries(rng, sum(n), 2 * group, 128)
+    mean = torch.from_numpy(rng.normal(size=(ref.k.shape[0], 2, 128))).float()
+    got = ba.cache_select(cache, q.cuda(), i32(offsets(n)), i32(lens), mean.cuda(), 64, 1, 6)
+    want = C.select(ref, f64(q), offsets(n), lens, f64(mean), 64, 1, 6)
+    assert np.array_equal(got.cpu().numpy(), C.words(want))
