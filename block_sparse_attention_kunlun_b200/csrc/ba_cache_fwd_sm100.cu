@@ -101,7 +101,8 @@ struct MmaShared {
 
 // What a block's roles know of its slots.
 struct Slots {
-    int32_t from;    // first slot (no list)
+    int32_t first;   // slots before it are seen by no row
+    int32_t from;    // first slot of the split (no list)
     int32_t shift;   // log2 of a unit's slots (no list: the whole tile is one)
     int32_t end;     // slots at and past it do not exist
     int32_t ntiles;
@@ -353,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
     if (!p.tree && !p.q.positions)
         sl.end = int32_t(min(int64_t(t.end), int64_t(t.len) + (t.row0 + t.rows - 1) / p.q.group + 1));
     const int32_t min_ws = sb.min_ws;
-    const int64_t from = first_slot(p, t, min_ws) / kKeys * kKeys + int64_t(split) * p.chunk;
+    sl.first = first_slot(p, t, min_ws);
+    const int64_t from = sl.first / kKeys * kKeys + int64_t(split) * p.chunk;
     int64_t to = split + 1 == p.nsplit ? sl.end : from + p.chunk;
     if (to > sl.end) to = sl.end;
     sl.from = int32_t(min(from, int64_t(sl.end)));
@@ -648,10 +650,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
             auto slot_of = [&](int32_t i) {
                 return sl.listed ? unit_slot(sl, sb, i, piece) : sl.from + i * kKeys + piece * slots;
             };
+            // (the first tile may begin with pages that no row needs and that may be gone)
+            auto wanted = [&](int32_t us) { return mine && us < sl.end && us + slots > sl.first; };
             auto entry_of = [&](int32_t i) -> int32_t { // page table entry, not checked yet
-                if (!mine || i >= sl.ntiles) return -1;
+                if (i >= sl.ntiles) return -1;
                 const int32_t us = slot_of(i);
-                return us < sl.end ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (us >> p.c.page_shift)) : -1;
+                return wanted(us) ? __ldg(p.c.page_table + int64_t(t.b) * p.c.max_pages + (us >> p.c.page_shift)) : -1;
             };
             int32_t next = entry_of(0), i = 0;
             for (; i < sl.ntiles; ++i) {
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_fwd_mma_kernel(const __grid
                 int32_t count = 0; // slots of the piece that there are
                 const int32_t us = slot_of(i);
                 if (uint32_t(id) < uint32_t(p.c.num_pages)) count = min(sl.end - us, slots);
-                else if (mine && us < sl.end) {
+                else if (wanted(us)) {
                     cache_range_error(p.c);
                     sb.holes = 1;
                 }

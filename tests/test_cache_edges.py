@@ -239,3 +239,22 @@ def test_select_of_one_and_two_rows_a_sequence(n, group):
     got = ba.cache_select(cache, q.cuda(), i32(offsets(n)), i32(lens), mean.cuda(), 64, 1, 6)
     want = C.select(ref, f64(q), offsets(n), lens, f64(mean), 64, 1, 6)
     assert np.array_equal(got.cpu().numpy(), C.words(want))
+
+
+@pytest.mark.parametrize("size", [16, 32, 128])
+@pytest.mark.parametrize("rows", ROWS)
+def test_pages_before_the_window_may_be_gone(rows, size):
+    """A history whose pages before every row's window were given back: no call needs them, none reports them."""
+    lens, block = [900], 48
+    cache, ref, rng = build(rows + size, [900 + rows], 2, 64, size)
+    gone = C.window_start(lens[0], block, 2) // size
+    assert gone > 0 and C.window_start(lens[0], block, 2) % 64 >= 48
+    cache.page_table[0, :gone] = -1
+    ref.table[0, :gone] = -1
+    q = queries(rng, rows, 2, 64)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32([0, rows]), i32(lens), block, 2)
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+    check(got, C.attend(ref, f64(q), [0, rows], lens, block, 2), 64)
+    cache.page_table[0, gone] = -1                       # one that is needed
+    ba.cache_attention_fwd(cache, q.cuda(), i32([0, rows]), i32(lens), block, 2)
+    assert ba.ba_device_status(cache.status) == ba.BA_ERR_INVALID_ARG
