@@ -47,7 +47,7 @@ __device__ __forceinline__ bool find_tile(const CacheFwd &p, int64_t number, int
 
 // One query row's view of the slots.
 struct RowView {
-    int32_t tok, pos, ws; // token within the sequence; nothing is visible for pos < 0
+    int32_t tok, pos, ws; // token within the sequence; for pos < 0 nothing is visible: ws past every slot
 };
 
 __device__ __forceinline__ RowView row_view(const CacheFwd &p, const FwdTile &t, int32_t row)
@@ -55,7 +55,7 @@ __device__ __forceinline__ RowView row_view(const CacheFwd &p, const FwdTile &t,
     RowView r;
     r.tok = row / p.q.group;
     r.pos = query_position(p.q, t.q0, t.len, r.tok);
-    r.ws = r.pos >= 0 ? rule_start(p.q, r.pos) : 0;
+    r.ws = r.pos >= 0 ? rule_start(p.q, r.pos) : INT32_MAX;
     return r;
 }
 

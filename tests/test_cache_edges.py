@@ -258,3 +258,28 @@ def test_pages_before_the_window_may_be_gone(rows, size):
     cache.page_table[0, gone] = -1                       # one that is needed
     ba.cache_attention_fwd(cache, q.cuda(), i32([0, rows]), i32(lens), block, 2)
     assert ba.ba_device_status(cache.status) == ba.BA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+def test_rows_at_negative_positions_ask_for_nothing(rows, selected):
+    """A row that sees nothing (a padded tree's) does not make its tile walk the history from the start: pages that
+    the other rows do not need may be gone."""
+    lens, block, n = [900, 900], 48, [rows, rows]
+    cache, ref, rng = build(rows, [900 + rows] * 2, 2, 64, 16)
+    gone = C.window_start(900, block, 2) // 16
+    keep = [7] if selected else []
+    drop = [c for c in range(gone) if c not in keep]
+    cache.page_table[:, drop] = -1
+    ref.table[:, drop] = -1
+    q = queries(rng, 2 * rows, 2, 64)
+    pos = [900 + t if t % 3 else -1 - t for t in range(rows)] + [-1] * rows
+    mask = None
+    if selected:
+        bits = np.zeros((2 * rows, 2, ref.table.shape[1]), dtype=bool)
+        bits[:, :, keep] = True
+        mask = C.words(bits)
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32(offsets(n)), i32(lens), block, 2, positions=i32(pos),
+                                 page_mask=None if mask is None else i32(mask))
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+    check(got, C.attend(ref, f64(q), offsets(n), lens, block, 2, pos, None, mask), 64)
