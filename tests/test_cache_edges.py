@@ -283,3 +283,45 @@ def test_rows_at_negative_positions_ask_for_nothing(rows, selected):
                                  page_mask=None if mask is None else i32(mask))
     assert ba.ba_device_status(cache.status) == ba.BA_OK
     check(got, C.attend(ref, f64(q), offsets(n), lens, block, 2, pos, None, mask), 64)
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+def test_a_tree_without_positions(rows, selected):
+    """tree_mask alone: row t is at position lens + t, and any bits count, those of later rows excepted."""
+    lens, n = [70, 333], [rows, max(1, rows - 2)]
+    cache, ref, rng = build(rows, [a + b for a, b in zip(lens, n)], 2, 128, 16)
+    total = sum(n)
+    q = queries(rng, total, 2, 128)
+    tree = C.words(rng.random((total, 64)) < 0.5)
+    mask = C.words(rng.random((total, 2, ref.table.shape[1])) < 0.2) if selected else None
+    got = ba.cache_attention_fwd(cache, q.cuda(), i32(offsets(n)), i32(lens), 32, 2, tree_mask=i32(tree),
+                                 page_mask=None if mask is None else i32(mask))
+    check(got, C.attend(ref, f64(q), offsets(n), lens, 32, 2, None, tree, mask), 128)
+    assert ba.ba_device_status(cache.status) == ba.BA_OK
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_captured_with_the_bindings_buffers_on_a_stream_of_the_capture(rows):
+    """Two branches of one graph, each a split call on an explicit stream with buffers from the binding."""
+    cache, _, rng = build(rows, [4000 + rows], 1, 128, 64)
+    q = [queries(rng, rows, 1, 128).cuda() for _ in "ab"]
+    offs, lens = i32([0, rows]), i32([4000])
+    want = [ba.cache_attention_fwd(cache, x, offs, lens, 1 << 20, 1) for x in q]
+    side = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = []
+        for s, x in zip(side, q):
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(ba.cache_attention_fwd(cache, x, offs, lens, 1 << 20, 1, stream=s))
+        for s in side:
+            torch.cuda.current_stream().wait_stream(s)
+    for _ in range(20):
+        for out, lse in got:
+            out.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
