@@ -69,7 +69,8 @@ __device__ __forceinline__ uint32_t div_heads(uint32_t x, uint32_t d, uint32_t m
 // only rounding. fmaxf drops NaN: a NaN leaves its block's scale alone and becomes E4M3's NaN;
 // an infinity gives e = 120 and the largest code.
 // Bound by HBM for many rows (each thread has kBatch loads under way): whole jagged histories
-// of 540,000 rows of 8 heads of 128 in bf16, 3.3 GB, in 561 us, 5.9 TB/s. By the launch for few.
+// of 540,000 rows of 8 heads of 128 in bf16, 3.3 GB, in 553 to 585 us, 5.7 to 6.0 TB/s. For few rows
+// by latency: one event for each of 256 histories takes 4.7 us within a captured step (9.2 with its call).
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_write_kernel(const CacheView c, const T *__restrict__ k, const T *__restrict__ v,
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kRowThreads)
 // D / 16 lanes hold a (row, head), sixteen values each: 16 bytes of codes in, 32 (bf16) or 64
 // bytes out. A bf16 result is exact (four significant bits) unless it falls below bf16's
 // normal range. Bound by HBM: 65,000 rows of 8 heads of 128 as bf16, 0.41 GB, in 71 us, 5.7
-// TB/s; as float32 (0.085 GB) 18 us, with 16-byte stores 25.
+// TB/s; as float32 (0.085 GB) 18 us (14 within a captured step), with 16-byte stores 25.
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_read_kernel(const CacheView c, const int32_t *__restrict__ row_offsets, const int32_t *__restrict__ starts,
@@ -273,9 +274,9 @@ cudaError_t launch_cache_read(const CacheView &c, bool f32, const int32_t *row_o
 // bytes a lane, eight loads at a time; each lane sums its sixteen columns over its rows in
 // float32 and the lanes that share columns are added at the end. The pages of a (sequence,
 // head) are dealt to `share` warps, as many as the GPU holds at 128 registers a thread. Bound by
-// one page's latency for few pages (9 us for one of each of 256 histories, most of it the
-// launch); for many by HBM: 0.29 GB of keys in 52 us, 5.6 TB/s (60 with each batch loaded after
-// the one before it was summed; 112 squeezed into 96 registers for more warps).
+// one page's latency for few pages (8.2 us for one of each of 256 histories, 7.2 within a captured
+// step); for many by HBM: 0.29 GB of keys in 50 to 55 us, 5.3 to 5.8 TB/s (60 with each batch loaded
+// after the one before it was summed; 112 squeezed into 96 registers for more warps).
 template <int D>
 __global__ void __launch_bounds__(128)
     cache_summarize_kernel(const CacheView c, const int32_t *__restrict__ starts, const int32_t *__restrict__ ends,
@@ -533,11 +534,13 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uin
 // roundings, and an absolute part for what underflows. A lane's four consecutive columns of
 // its two pages are its columns of an MMA step, so the means go from memory to the MMAs
 // through registers alone. (Float32 on the CUDA cores, one page a lane, means through shared
-// memory and a tighter band: 45 us where this takes 28, for 8 trees of 17 to 64 rows over
-// 16,000 to 33,000 events in 64-slot pages, 8 heads of 128, the 32 best pages.) Bound by the
-// chain of a block's latencies: offsets, page numbers, means, then the choice, some 8 us of
-// the 28. Three blocks of eight rows an SM, at the price of a few spilled registers: with two
-// 32 us. Rows go to blocks of four warps one by one (eight: 15.5 for 14.0 us, 64 histories).
+// memory and a tighter band: 45 us where this takes 27, for 8 trees of 17 to 64 rows over
+// 16,000 to 33,000 events in 64-slot pages, 8 heads of 128, the 32 best pages.) No unit is busy
+// half of the time there. Offsets, page numbers, means and the choice follow one another in each
+// block, some 8 us of the 27; and every block of eight rows reads all candidates' means of its
+// sequence and head again, some 70 MB through L2 where 12.5 MB differ. Three blocks of eight rows
+// an SM (up to some 1100 pages, whose keys take 70 KB a block), at the price of a few spilled registers:
+// with two 32 us. Rows go to blocks of four warps one by one (eight: 15.5 for 14.0 us, 64 histories).
 template <int D, int kRows>
 __global__ void __launch_bounds__(select_warps(kRows) * 32, kRows > 1 ? 3 : 4)
     cache_select_kernel(const CacheView c, const CacheQuery q, const float *__restrict__ summaries, int32_t topk,

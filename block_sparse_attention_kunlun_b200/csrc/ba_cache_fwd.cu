@@ -39,10 +39,12 @@ __host__ __device__ constexpr int simt_blocks(int head_dim) { return head_dim ==
 // The sets and the warps are joined once at the end.
 // Values are on their way while scores are formed, the next slots' keys while values are added.
 // One event over the windows of 256 histories (8 heads of 128, up to 512 slots each, 0.20 GB):
-// 47 us, 4.3 TB/s, of which some 4 us go to the launch and, in each of a block's rounds, 2
-// to 3 to finding its sequence and pages before the first keys are under way; over windows of
-// 4096 slots 223 us. Five blocks an SM (four, without a bound on registers: 50 and 228; six or
-// seven spill: 61 and 300); at D = 64, with half the codes a lane, seven (30 us; five 35).
+// 47 us, 4.3 TB/s (44 within a captured step), of which some 4 us go to the launch and, in each of a
+// block's rounds, 2 to 3 to finding its sequence and pages before the first keys are under way; over
+// windows of 4096 slots, whole histories mostly (1.1 GB), 213 us, and over 4096 slots of each (2.2 GB)
+// 348, 6.4 TB/s. With 32 selected pages of 64 for each of 16 long histories (0.08 GB) 31 us: a split is
+// a stretch of slots, whatever pages in it are selected. Five blocks an SM (four, without a bound on registers: 50 and 228 where five took 47 and 223;
+// six or seven spill: 61 and 300); at D = 64, with half the codes a lane, seven (30 to 32 us; five 35).
 // Splitting the windows further (two, three parts) takes 12% and 21% more.
 template <int D>
 __global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D)) cache_fwd_simt_kernel(const CacheFwd p)
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D)) cache_fwd_sim
 
 // Joins the splits of every (row, head): weights 2^(m_s - max m), in the order of the splits.
 // One warp per row and head, D / 32 columns a lane; bound by its launch and the latency of
-// its reads (some 5 us of the 115 of 16 candidate sets in four splits).
+// its reads (some 5 us of the 113 to 116 of 16 candidate sets in four splits).
 template <int D>
 __global__ void __launch_bounds__(256) cache_combine_kernel(const CacheFwd p)
 {
@@ -276,6 +278,13 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
     // sequence counts for less than the rows that one token brings
     const int64_t live = batch < rows ? batch : rows;
     const int64_t each = live > 0 ? (all + live - 1) / live : 1;
+    // The kernel goes by the rows of a sequence on average. (us for tiles of 8, 16, 128 rows, trees of so many
+    // rows. 64 windows of four 512: 8 rows 71, 103, 114; 12 124, 105, 115; 16 123, 109, 116; 17 -, 165, 117;
+    // 32 -, 176, 121. 8 whole histories of 16,000 to 33,000: 8 rows 122, 159, 191; 12 196, 161, 192; 16 200,
+    // 162, 192; 17 -, 255, 192; 32 -, 270, 195. One event, 16 whole histories of 25,000 to 33,000, on the
+    // CUDA cores, 8, 16: one head 163, 227, 296; two 287, 224, 297; four 546, 222, 296.) A batch of unlike
+    // sequences pays for that: 255 single events over windows take 44 us and a chunk of 512 rows 21, together,
+    // in tiles of 8 rows, 87 (under four heads 63, 33 and, in tiles of 16, 169).
     plan.tile_rows = each <= 1 ? 1 : (each <= 8 ? 8 : (each <= 16 ? 16 : kMmaRows));
     const bool mma = plan.tile_rows == kMmaRows;
     plan.tiles = plan.tile_rows > 1 ? all / plan.tile_rows + batch : all;
@@ -285,12 +294,15 @@ CacheFwdPlan cache_fwd_plan(int32_t batch, int32_t rows, int32_t kv_heads, int32
         const int64_t per = live > 0 ? (int64_t(rows) + live - 1) / live : 0;
         if (window < slots && block < slots && block * window + per < slots) reach = block * window + per;
     }
-    // Splits: as many as fill the blocks that 148 SMs hold at once (some more would leave most SMs
-    // waiting for the rest), or three times that (twice on the tensor cores, whose blocks take
-    // longer to set up) where a split still has 1024 slots, none of fewer than 256. (Three rounds,
-    // two, one: one event over 16 long histories under four heads 223, 233, 264 us, under sixteen
-    // 310, 333, 352, more rounds no less; one row over 8 of them 60 each; 16 candidate sets with
-    // selected pages 130, 118, 116; 8 trees over windows, in splits of fewer slots, 44, 44, 34.)
+    // Splits: as many as fill the blocks that a B200's 148 SMs hold at once (a constant: the workspace query
+    // must say the same without a device), or three times that (twice on the tensor cores) where a split
+    // still has 1024 slots, none of fewer than 256. With more items than places nothing is split, and
+    // the last round of blocks is as full as it happens to be. (us for three rounds, two, one. One event
+    // over 16 histories of 25,000 to 33,000: four heads 215, 222, 256, sixteen 309, 333, 349, one 166, 172, 197;
+    // over two, four heads, 43 each. On the tensor cores, where no one of them is best: 16 candidate sets with
+    // selected pages 115, 109, 118; 8 trees over whole histories 194, 182, 195; 32 of 64 rows over 8192 slots
+    // 263, 252, 230; 16 chunks of 128 to 512 rows over windows 143, 117, 117; one of 512 over 32,768 slots
+    // 166, 145, 130; 8 or 64 trees over windows, in splits of fewer slots or none, alike.)
     const int64_t held = 148 * (mma ? 2 : plan.tile_rows == 1 ? simt_blocks(head_dim) : plan.tile_rows == 8 ? 4 : 3);
     const int64_t work = (all + plan.tile_rows - 1) / plan.tile_rows;
     const int64_t items = (work > live ? work : live) * kv_heads;

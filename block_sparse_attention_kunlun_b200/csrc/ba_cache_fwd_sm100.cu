@@ -11,7 +11,9 @@
 // value has four significant bits and the scale is a power of two) and store them in the
 // MMA's 128-byte-swizzled layout. A tensor product on the codes themselves would have to round Q
 // to E4M3, and the values' scales run along head_dim, not along the keys that P V sums over.
-// P is rounded to bf16 for its MMA, the running sum takes the unrounded probabilities.
+// P is rounded to bf16 for its MMA, as in ba_fwd; the running sum takes the unrounded probabilities. (out is
+// then off by 0.0019 of its size, root mean square, where its own rounding makes 0.0016. P in two bf16 parts
+// would end at 0.0016, with twice the MMAs of P V: 140 us for the trees below, 123 for the candidates.)
 //
 // Roles of a block (512 threads, two blocks an SM, so that one block's softmax and set-up
 // overlap the other's MMAs):
@@ -25,8 +27,9 @@
 // Columns are kept in the order that widening four codes at once gives, 0 2 1 3 within each
 // four: Q is put in the same order as it is loaded, O is put back as it is stored.
 //
-// 64 trees of 5 to 64 rows over windows of four blocks of 512 (8 heads of 128, 0.25 GB): 124 us;
-// 16 sets of 33 to 64 candidates with 32 selected pages a row (group of two, 0.12 GB): 115 us.
+// 64 trees of 5 to 64 rows over windows of four blocks of 512 (8 heads of 128, 0.25 GB): 124 to 126 us;
+// 16 sets of 33 to 64 candidates with 32 selected pages a row (group of two, 0.12 GB): 113 to 116 us;
+// 16 chunks of 512 rows over such windows: 143 us, 420 TFLOP/s.
 // Not bytes but the chain of a tile bounds it, which the two blocks of an SM overlap by half.
 // Clocked in the first case, in cycles: S's eight MMAs take 340 to issue and 330 more to finish,
 // S's load 260, the maximum 130, the exponentials 710, storing P 135, the hand-over 90, P V's MMAs

@@ -15,15 +15,19 @@
 //   O^T [16 columns x 8 rows] += V^T P^T: a lane reads 16 consecutive codes of four slots and
 //       pairs them slot by slot; which of the output's rows stands for which column is free
 //       too. P^T comes from S^T by movmatrix.
-// Codes are widened to bf16, exactly (as in ba_cache_fwd_sm100.cu); P is rounded to bf16. Values
+// Codes are widened to bf16, exactly (as in ba_cache_fwd_sm100.cu); P is rounded to bf16, as in ba_fwd
+// (its sum is not): out is then off by 0.0019 to 0.0020 of its size (root mean square) where its own
+// rounding to bf16 makes 0.0016. P in two bf16 parts, with twice the MMAs of P V, would end at 0.0016
+// and take 5% longer under four heads, 7% under sixteen. Values
 // are on their way while S is formed, the next slots' keys while P V is. Slots with codes that the
 // widening does not know (NaN, scales past 2^7) get their scores, and their values, put in in
 // float32 after the MMAs: everything else stays the same to the bit.
 //
-// The case above: 0.97 GB in 223 us, 4.3 TB/s; with sixteen query heads 313. Bound by the
-// integer pipe and by issue: to put a code's bits into a bf16's places takes four integer
-// operations for two codes, over half of the integer pipe's time and two thirds of all issue
-// slots, with loads between them. (NaN looked for in the codes ahead of the MMAs: 234 and
+// The case above: 0.97 GB in 219 to 229 us, 4.2 to 4.4 TB/s; with sixteen query heads 302 to 313. No unit
+// is busy all the time: ncu has the integer pipe at 58%, issue at 59% and DRAM at 54%, with 22% of an SM's
+// warps. To put a code's bits into a bf16's places takes four integer operations for two codes, the most of the
+// integer pipe's time, with loads and MMAs that wait for one another between them. (NaN looked for in the codes
+// ahead of the MMAs: 234 and
 // 351; a step's loads all at once: 240 and 411; widened by the float16 conversion instruction:
 // 285; with the pages brought into L2 ahead: 267.)
 #include "ba_cache_fwd.cuh"

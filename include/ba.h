@@ -480,7 +480,14 @@ ba_status ba_cache_select(const ba_cache *cache, const ba_problem *problem, cons
  * infinity included, does not reach it. Queries at negative positions see
  * nothing.
  *
- * BF16 only; head_dim 64 or 128. Workspace: ba_cache_fwd_workspace_size
+ * Positions may be any: a row need not stand at the position of its slot. A
+ * page that no row of the sequence can see, before all their windows and not
+ * selected, is not asked for and may be gone.
+ *
+ * BF16 only; head_dim 64 or 128. Scores, softmax and sums are formed in
+ * float32; where the plan takes two rows or more of a sequence and key/value
+ * head at once, the probabilities are rounded to bf16 before they meet the
+ * values (their sum is not), as in ba_fwd. Workspace: ba_cache_fwd_workspace_size
  * bytes, enough with and without page_mask (it may be 0, and workspace
  * NULL); it depends on the sizes in the two structs, block and window, not
  * on the lengths. Results do not depend on timing or on earlier calls.
