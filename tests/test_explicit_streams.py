@@ -77,3 +77,23 @@ def test_results_on_an_explicit_stream(kind):
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_streams_by_number():
+    """CUDA's default streams by their numbers, a stream by its handle, and calls without rows."""
+    offs = torch.tensor([0, 5, 90], dtype=torch.int32).cuda()
+    q = torch.randn((90, 2, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    want = ba.block_attention_fwd(q, q, q, offs, 16, 2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (0, 1, 2, side.cuda_stream, side, torch.cuda.default_stream()):
+        out, lse = ba.block_attention_fwd(q, q, q, offs, 16, 2, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        out, _ = ba.block_attention_fwd(q[:0], q[:0], q[:0], offs * 0, 16, 2, stream=stream)
+        assert out.shape == (0, 2, 64)
+    with torch.cuda.stream(side):   # the caller's stream is the call's
+        out, lse = ba.block_attention_fwd(q, q, q, offs, 16, 2, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want[0])
