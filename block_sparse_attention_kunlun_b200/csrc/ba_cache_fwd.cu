@@ -43,8 +43,9 @@ __host__ __device__ constexpr int simt_blocks(int head_dim) { return head_dim ==
 // block's rounds, 2 to 3 to finding its sequence and pages before the first keys are under way; over
 // windows of 4096 slots, whole histories mostly (1.1 GB), 213 us, and over 4096 slots of each (2.2 GB)
 // 348, 6.4 TB/s. With 32 selected pages of 64 for each of 16 long histories (0.08 GB) 31 us: a split is
-// a stretch of slots, whatever pages in it are selected. Five blocks an SM (four, without a bound on registers: 50 and 228 where five took 47 and 223;
-// six or seven spill: 61 and 300); at D = 64, with half the codes a lane, seven (30 to 32 us; five 35).
+// a stretch of slots, whatever pages in it are selected. Five blocks an SM (four, without a bound on
+// registers: 50 and 228 us where five took 47 and 223; six or seven spill: 61 and 300); at D = 64, with
+// half the codes a lane, seven (30 to 32 us; five 35).
 // Splitting the windows further (two, three parts) takes 12% and 21% more.
 template <int D>
 __global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D)) cache_fwd_simt_kernel(const CacheFwd p)
